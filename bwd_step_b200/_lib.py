@@ -20,6 +20,11 @@ NC_ERR_CUDA = -4
 NC_ERR_BAD_TOKEN = -5
 NC_ERR_DEVICE_TIMEOUT = -6
 NC_ERR_NO_DEVICE = -7
+NC_ERR_OUT_OF_PAGES = -8
+NC_ERR_BAD_LENGTH = -9
+NC_ERR_BAD_PAGE = -10
+
+NC_MAX_BEAMS = 32
 
 NC_RECOMPUTE_NONE = 0
 NC_RECOMPUTE_MLP = 1
@@ -81,6 +86,15 @@ SIGNATURES = {
     "nc_inference_workspace_bytes": (_SZ, [_P, _I, _I]),
     "nc_prefill": (_I, [_P, _P, _I, _I, _P, _P, _I, _P, _P, _SZ, _P]),
     "nc_decode_step": (_I, [_P, _P, _I, _I, _P, _P, _I, _P, _P, _SZ, _P]),
+    "nc_paged_kv_bytes": (_SZ, [_P, _I, _I]),
+    "nc_page_plan": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "nc_paged_attention_workspace_bytes": (_SZ, [_P, _I, _I]),
+    "nc_paged_attention": (_I, [_P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "nc_paged_workspace_bytes": (_SZ, [_P, _I, _I]),
+    "nc_paged_forward": (_I, [_P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "nc_beam_select": (_I, [_P, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "nc_beam_reorder": (_I, [_P, _P, _I, _I, _I, _P, _I, _I, _P]),
+    "nc_beam_reorder_paged": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _I, _P, _P, _P]),
     "nc_adamw_step": (_I, [ctypes.POINTER(NcAdamwGroup), _I, ctypes.c_int64, _I, _P, _P, _I, _P, _P, _P, _P]),
     "nc_gemm_wgrad_noalloc": (_I, [_I, _I, _I, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _I, _P, _P]),
     # include/nanochat_b200_testing.h

@@ -16,8 +16,10 @@ enum DType : int { DT_F32 = 0, DT_BF16 = 1 };
 inline size_t dt_size(DType t) { return t == DT_BF16 ? 2 : 4; }
 
 // ---------------------------------------------------------------- memory-bound
-// cos/sin [T, hd/2] of pos * base^(-2j/hd) for pos = pos0 .. pos0 + T - 1, evaluated in double.
-cudaError_t launch_rope_table(float* cos_t, float* sin_t, int T, int hd, float base, cudaStream_t s, int pos0 = 0);
+// cos/sin [T, hd/2] of pos * base^(-2j/hd) for pos = pos0 .. pos0 + T - 1, or for the T device
+// positions, evaluated in double.
+cudaError_t launch_rope_table(float* cos_t, float* sin_t, int T, int hd, float base, cudaStream_t s, int pos0 = 0,
+                              const int32_t* positions = nullptr);
 
 // x[m] = rmsnorm(wte[idx[m]]) (fp32 residual stream), r0[m] = its inverse RMS.
 cudaError_t launch_embed_norm_fwd(DType wt, const int32_t* idx, const void* wte, int M, int V, int d,

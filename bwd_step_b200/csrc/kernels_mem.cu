@@ -26,11 +26,12 @@ constexpr int kRowWarps = 8;  // rows per 256-thread block
 inline int row_blocks(int M) { return (M + kRowWarps - 1) / kRowWarps; }
 
 // ---------------------------------------------------------------- RoPE table
-__global__ void rope_table_kernel(float* c, float* s, int T, int hd, double base, int pos0) {
+__global__ void rope_table_kernel(float* c, float* s, int T, int hd, double base, int pos0,
+                                  const int32_t* __restrict__ positions) {
     int half = hd / 2;
     int i = blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= T * half) return;
-    int pos = pos0 + i / half, j = i % half;
+    int pos = positions ? positions[i / half] : pos0 + i / half, j = i % half;
     double theta = pow(base, -2.0 * (double)j / (double)hd);
     double ang = (double)pos * theta;
     c[i] = (float)cos(ang);
@@ -1030,9 +1031,10 @@ __global__ void expired_wait_kernel(int* status, int max_iters) {
 std::atomic<long long> g_launches{0};
 
 // ============================================================================ launchers
-cudaError_t launch_rope_table(float* c, float* s, int T, int hd, float base, cudaStream_t st, int pos0) {
+cudaError_t launch_rope_table(float* c, float* s, int T, int hd, float base, cudaStream_t st, int pos0,
+                              const int32_t* positions) {
     int n = T * (hd / 2);
-    rope_table_kernel<<<(n + 255) / 256, 256, 0, st>>>(c, s, T, hd, (double)base, pos0);
+    rope_table_kernel<<<(n + 255) / 256, 256, 0, st>>>(c, s, T, hd, (double)base, pos0, positions);
     count_launch();
     return cudaGetLastError();
 }

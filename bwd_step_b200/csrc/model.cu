@@ -6,58 +6,15 @@
 // token embedding -> n_layer pre-norm blocks [x += Wo attn(rope(norm(q)),
 // rope(norm(k)), v); x += Wproj relu(Wfc norm(x))^2] -> final norm -> untied
 // LM head -> tanh softcap -> mean next-token cross-entropy.
-#include "nanochat_b200.h"
+#include "model.h"
 #include "common.cuh"
-#include "kernels.h"
 #include "gemm_tc.h"
 #include "attention_tc.h"
+#include "paged.h"
 
-#include <string>
-#include <vector>
 #include <algorithm>
 
 using namespace nc;
-
-struct ParamEntry { std::string name; int64_t offset; int rows, cols; };
-
-struct nc_model {
-    nc_config cfg;
-    nc_precision prec;
-    int device = 0;
-    int* status = nullptr;  // device int[64]: [0] = status flags, [1] = loss scratch for the host variant
-    std::vector<ParamEntry> layout;
-    int64_t nparams = 0;
-    int V, d, L, H, nkv, hd, F, Nqkv;
-    DType at;  // weight / activation type
-    bool tc = false;  // tcgen05 path available (bf16 on sm_100)
-    // LM head: fused (logits never stored; tensor-core path only) or materialised
-    // logit chunks with a separate cross-entropy pass; rows per chunk (0 = default)
-    int lm_mode = NC_LM_HEAD_FUSED;
-    int lm_rows = 0;
-    // activations recomputed in the backward instead of saved (NC_RECOMPUTE_*)
-    int recompute = NC_RECOMPUTE_NONE;
-    // caller-owned events recorded when each gradient bucket is final (may be empty)
-    std::vector<cudaEvent_t> grad_events;
-    // the backward's weight-gradient GEMMs run on this second stream, overlapping the
-    // input-gradient chain on the caller's stream; kSideEvents order the two (null: off)
-    static constexpr int kSideEvents = 6;
-    cudaStream_t side = nullptr;
-    cudaEvent_t sev[kSideEvents] = {};
-    // profiler: CUDA events around every launch while enabled
-    struct Rec { int cls; cudaEvent_t a, b; double flops, bytes; long long launches; };
-    bool prof_on = false;
-    std::vector<cudaEvent_t> ev_pool;
-    size_t ev_next = 0;
-    std::vector<Rec> recs;
-    cudaEvent_t event() {
-        if (ev_next == ev_pool.size()) {
-            cudaEvent_t e = nullptr;
-            if (cudaEventCreate(&e) != cudaSuccess) return nullptr;
-            ev_pool.push_back(e);
-        }
-        return ev_pool[ev_next++];
-    }
-};
 
 namespace {
 
@@ -318,6 +275,13 @@ struct KvCache {
     int T_max, pos;
     bool decode;
     size_t layer_bytes;  // K + V of one layer
+    // a paged step (paged != null): its tables (k, v unset), the rows' slots and positions, the
+    // attention's workspace and the bound of a request's new rows
+    const PagedKv* paged = nullptr;
+    const int32_t* slots = nullptr;
+    const int32_t* positions = nullptr;
+    void* attn_ws = nullptr;
+    int max_new = 0;
     void* k(int l) const { return base + (size_t)l * layer_bytes; }
     void* v(int l) const { return base + (size_t)l * layer_bytes + layer_bytes / 2; }
 };
@@ -336,7 +300,7 @@ int forward_blocks(const Ctx& c, const W& w, const int32_t* tok, bool save, cons
     {
         Prof pr(c, P_OTHER, 0.0, 8.0 * c.p.T * (m->hd / 2));
         CK(launch_rope_table(c.at<float>(c.p.cosb), c.at<float>(c.p.sinb), c.p.T, m->hd, m->cfg.rope_base, c.s,
-                             decode ? kv->pos : 0));
+                             decode ? kv->pos : 0, kv ? kv->positions : nullptr));
     }
     const double A = (double)dt_size(m->at);
     { Prof pr(c, P_EMBED_FWD, 0.0, (double)M * (A * d + 4.0 * d + 8.0)); CK(launch_embed_norm_fwd(m->at, tok, w.wte(), M, m->V, d, x, c.at<float>(c.p.r0), m->status, c.s)); }
@@ -370,12 +334,21 @@ int forward_blocks(const Ctx& c, const W& w, const int32_t* tok, bool save, cons
             Prof pr(c, P_QKROPE_FWD, 0.0, (double)M * (m->H + m->nkv) * (2.0 * A * m->hd + 4.0));
             CK(launch_qknorm_rope_fwd(m->at, qkv, rqk, cs, sn, M, c.p.T, m->H, m->nkv, m->hd, c.s));
         }
-        if (kv) {
+        if (kv && kv->paged) {
+            Prof pr(c, P_ATTN_FWD, 0.0, 0.0);
+            PagedKv pk = *kv->paged;
+            pk.k = kv->k(l);
+            pk.v = kv->v(l);
+            CK(paged_attention(m->at, qkv, m->H, m->nkv, m->hd, M, kv->max_new, kv->slots, pk, o, kv->attn_ws,
+                               m->status, c.s));
+        } else if (kv) {
             Prof pr(c, P_OTHER, 0.0, 4.0 * A * M * m->nkv * m->hd);
             CK(launch_kv_append(m->at, qkv, m->H, m->nkv, m->hd, M, c.p.T, decode ? kv->pos : 0, kv->k(l), kv->v(l),
                                 kv->T_max, c.s));
         }
-        if (decode) {
+        if (kv && kv->paged) {
+            // done above
+        } else if (decode) {
             Prof pr(c, P_ATTN_FWD, 4.0 * M * m->H * (double)m->hd * (kv->pos + 1), 0.0);
             CK(launch_decode_attention(m->at, qkv, kv->k(l), kv->v(l), kv->T_max, kv->pos + 1, c.p.B, m->H, m->nkv,
                                        m->hd, o, c.s));
@@ -569,13 +542,6 @@ int step(nc_model* m, const int32_t* tok, const int32_t* tgt, int B, int T, cons
     }
     RG(bucket_done(m->L + 1));  // dWte
     return NC_OK;
-}
-
-// The model's device must be current: its buffers are that device's memory,
-// and kernels launched on another device would reach them as peer memory.
-bool on_model_device(const nc_model* m) {
-    int dev = -1;
-    return cudaGetDevice(&dev) == cudaSuccess && dev == m->device;
 }
 
 int validate_call(nc_model* m, int B, int T, size_t ws_bytes, const void* const* ptrs, int nptr,
@@ -772,6 +738,45 @@ int nc_decode_step(nc_model* m, const int32_t* tokens, int B, int pos, const voi
     return cudaGetLastError() == cudaSuccess ? NC_OK : NC_ERR_CUDA;
 }
 
+size_t nc_paged_workspace_bytes(const nc_model* m, int n_req, int rows) {
+    if (!m || rows <= 0 || rows > (1 << 24)) return 0;
+    const size_t attn = nc_paged_attention_workspace_bytes(m, n_req, rows);
+    if (attn == 0) return 0;
+    return make_plan(m, 1, rows, true).total + al256((size_t)n_req * m->d * dt_size(m->at)) + al256(attn);
+}
+
+int nc_paged_forward(nc_model* m, const int32_t* tokens, int rows, int n_req, int max_new, const int32_t* positions,
+                     const int32_t* cu_rows, const int32_t* kv_len, const int32_t* slots, const int32_t* block_table,
+                     int max_blocks, int page_size, int n_pages, const void* weights, void* kv_pages, void* logits,
+                     void* workspace, size_t ws_bytes, void* stream) {
+    const void* ptrs[] = {tokens, positions, cu_rows, kv_len, slots, block_table, weights, kv_pages, logits, workspace};
+    int v = check_paged_step(n_req, rows, max_new, max_blocks, page_size, n_pages);
+    if (v != NC_OK) return v;
+    v = validate_call(m, 1, rows, ws_bytes, ptrs, 10, true);
+    if (v != NC_OK) return v;
+    if ((reinterpret_cast<uintptr_t>(kv_pages) & 15) || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return NC_ERR_INVALID_ARG;
+    if (ws_bytes < nc_paged_workspace_bytes(m, n_req, rows)) return NC_ERR_WORKSPACE_TOO_SMALL;
+    Ctx c{m, make_plan(m, 1, rows, true), (char*)workspace, (cudaStream_t)stream};
+    W w{(const char*)weights, dt_size(m->at), m};
+    char* last = c.ws + c.p.total;
+    const PagedKv pk{nullptr, nullptr, block_table, cu_rows, kv_len, n_req, max_blocks, page_size, n_pages};
+    KvCache kv{(char*)kv_pages, 0, 0, false, nc_paged_kv_bytes(m, n_pages, page_size) / m->L};
+    kv.paged = &pk;
+    kv.slots = slots;
+    kv.positions = positions;
+    kv.attn_ws = last + al256((size_t)n_req * m->d * dt_size(m->at));
+    kv.max_new = max_new;
+    RG(forward_blocks(c, w, tokens, false, &kv));
+    {
+        Prof pr(c, P_OTHER, 0.0, 2.0 * n_req * (double)m->d * dt_size(m->at));
+        CK(launch_last_rows(m->at, c.at(c.p.xf), m->d, rows, cu_rows, n_req, last, c.s));
+    }
+    RG(run_gemm(c, mk(m, n_req, m->V, m->d, last, m->d, true, w.wlm(), m->d, true, EPI_SOFTCAP, logits, m->V, m->at),
+                P_GEMM_LM_Z));
+    return cudaGetLastError() == cudaSuccess ? NC_OK : NC_ERR_CUDA;
+}
+
 int nc_check(nc_model* m, void* stream) {
     if (!m) return NC_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
@@ -782,6 +787,9 @@ int nc_check(nc_model* m, void* stream) {
     if (st & ST_TIMEOUT) return NC_ERR_DEVICE_TIMEOUT;
     if (st & ST_BAD_LAYOUT) return NC_ERR_CUDA;
     if (st & ST_BAD_TOKEN) return NC_ERR_BAD_TOKEN;
+    if (st & ST_BAD_LENGTH) return NC_ERR_BAD_LENGTH;
+    if (st & ST_OUT_OF_PAGES) return NC_ERR_OUT_OF_PAGES;
+    if (st & ST_BAD_PAGE) return NC_ERR_BAD_PAGE;
     return NC_OK;
 }
 
@@ -795,6 +803,9 @@ const char* nc_status_string(int code) {
         case NC_ERR_BAD_TOKEN: return "token or target id out of range";
         case NC_ERR_DEVICE_TIMEOUT: return "bounded device wait expired";
         case NC_ERR_NO_DEVICE: return "no sm_100 CUDA device";
+        case NC_ERR_OUT_OF_PAGES: return "not enough free pages";
+        case NC_ERR_BAD_LENGTH: return "length, row count or back-pointer out of range";
+        case NC_ERR_BAD_PAGE: return "page or slot outside the paged cache";
     }
     return "unknown status";
 }

@@ -47,6 +47,10 @@ extern "C" {
 #define NC_ERR_BAD_TOKEN           -5  /* device: a token or target id outside [0, V)    */
 #define NC_ERR_DEVICE_TIMEOUT      -6  /* device: a bounded wait in a kernel gave up     */
 #define NC_ERR_NO_DEVICE           -7  /* no sm_100 device current when the model was made */
+#define NC_ERR_OUT_OF_PAGES        -8  /* device: a step needs more pages than are free      */
+#define NC_ERR_BAD_LENGTH          -9  /* device: a length, row count or back-pointer out of
+                                          range                                           */
+#define NC_ERR_BAD_PAGE           -10  /* device: a page or slot outside the paged cache    */
 
 /* Parameter-free RMSNorm epsilon: y = x / sqrt(mean(x^2) + NC_RMS_EPS).  The
  * pages give no value; 1e-6 is used everywhere (token-embedding norm, the two
@@ -142,8 +146,9 @@ int nc_forward_logits(nc_model* m, const int32_t* tokens, int B, int T, const vo
                       void* logits, void* workspace, size_t ws_bytes, void* stream);
 
 /* Synchronises `stream`, then returns and clears the device status word:
- * NC_OK, NC_ERR_BAD_TOKEN or NC_ERR_DEVICE_TIMEOUT (or NC_ERR_CUDA if the
- * stream reported an error). */
+ * NC_OK, NC_ERR_BAD_TOKEN, NC_ERR_DEVICE_TIMEOUT, NC_ERR_OUT_OF_PAGES,
+ * NC_ERR_BAD_LENGTH or NC_ERR_BAD_PAGE (or NC_ERR_CUDA if the stream reported
+ * an error). */
 int nc_check(nc_model* m, void* stream);
 
 /* Static description of a return code. */
@@ -215,6 +220,123 @@ int nc_prefill(nc_model* m, const int32_t* tokens, int B, int T, const void* wei
                void* logits, void* workspace, size_t ws_bytes, void* stream);
 int nc_decode_step(nc_model* m, const int32_t* tokens, int B, int pos, const void* weights, void* kv_cache,
                    int T_max, void* logits, void* workspace, size_t ws_bytes, void* stream);
+
+/* Inference over a paged KV cache: requests of different lengths in one step,
+ * each with a chunk of new tokens (its prompt, a part of it, one decoded token,
+ * or none).  The cache of one layer is K and V, each [n_pages, page_size,
+ * n_kv_head, head_dim] in the weights' type (K after QK-norm and RoPE); the
+ * cache of a model is [n_layer] x {K, V} of those, nc_paged_kv_bytes bytes.
+ * Position p of request r is kept in slot
+ *   block_table[r][p / page_size] * page_size + p % page_size.
+ * page_size: 16, 32, 64, 128 or 256.  block_table: device int32 [n_req,
+ * max_blocks], -1 (or any value outside [0, n_pages)) where a block has no
+ * page.  n_req <= 4096; max_blocks * page_size and n_pages * page_size at most
+ * 2^30.  A position that a step writes must be in a page of its own: requests
+ * may share a page only where none of them writes.
+ *
+ * nc_page_plan builds what a step of n_req requests needs from their lengths, on
+ * the GPU:
+ *   cached_len, new_len: device int32 [n_req], positions in the cache and new
+ *     positions of this step (both >= 0).
+ *   release: device int32 [n_req] or NULL; where not 0, the request's pages are
+ *     given back first (every page in its table row; a page in the rows of two
+ *     released requests would be given back twice) and it starts anew with 0
+ *     cached positions.
+ *   block_table (in/out), free_pages [n_pages] and free_count [1] (in/out): the
+ *     free pages as a stack, its top last.  Released pages are pushed in the
+ *     order of requests and blocks, then every block of [cached_len,
+ *     cached_len + new_len) without a page takes one from the top, in that
+ *     order.  Blocks that have a page keep it, so planning a step twice changes
+ *     nothing.
+ *   cu_rows [n_req + 1]: packed row of every request's first new token, and the
+ *     number of rows in use; kv_len [n_req]: cached + new (may be cached_len's
+ *     own buffer).
+ *   positions, slots [rows]: position and cache slot of every packed row; 0 and
+ *     -1 for rows behind the last request's.
+ * Lengths that are negative, longer than the table, or more rows than `rows`
+ * (NC_ERR_BAD_LENGTH), or too few free pages (NC_ERR_OUT_OF_PAGES), refuse the
+ * step as a whole: table, stack and count stay as they were, cu_rows is 0, slots
+ * are -1, kv_len is cached_len, and nc_check reports it.  A free page outside
+ * [0, n_pages) gives its positions the slot -1 and is reported as
+ * NC_ERR_BAD_PAGE. */
+size_t nc_paged_kv_bytes(const nc_model* m, int n_pages, int page_size);
+int nc_page_plan(nc_model* m, int n_req, int page_size, int max_blocks, int n_pages, int rows,
+                 const int32_t* cached_len, const int32_t* new_len, const int32_t* release, int32_t* block_table,
+                 int32_t* free_pages, int32_t* free_count, int32_t* cu_rows, int32_t* kv_len, int32_t* positions,
+                 int32_t* slots, void* stream);
+
+/* Attention of the requests' new tokens over one layer's paged cache.
+ *   qkv: device [rows, (n_head + 2 n_kv_head) head_dim], packed rows as the fused
+ *     projection leaves them after QK-norm and RoPE; cu_rows, kv_len, slots as
+ *     nc_page_plan writes them.
+ *   First the k, v heads of every row are written to its slot (rows with slot
+ *   < 0 have none), then row i of request r, at position
+ *   p = kv_len[r] - cu_rows[r + 1] + i, attends to positions 0..p:
+ *   o[i] = softmax(q K^T / sqrt(head_dim)) V into o [rows, n_head head_dim].
+ *   Rows from cu_rows[n_req] on are left as they were.
+ *   max_new: an upper bound of every request's number of new rows, 0 if none is
+ *   known (it chooses the kernels, the results do not depend on it).
+ *   workspace: nc_paged_attention_workspace_bytes(m, n_req, rows) bytes,
+ *   256-byte aligned; contents on entry are ignored.
+ * A block without a page inside a request's length reads as zeros and is
+ * reported as NC_ERR_BAD_PAGE.  Cache contents past a request's length are not
+ * used, whatever they are.  Results are bitwise reproducible for the same
+ * lengths. */
+size_t nc_paged_attention_workspace_bytes(const nc_model* m, int n_req, int rows);
+int nc_paged_attention(nc_model* m, const void* qkv, int rows, int n_req, int max_new, const int32_t* cu_rows,
+                       const int32_t* kv_len, const int32_t* slots, const int32_t* block_table, int max_blocks,
+                       int page_size, int n_pages, void* k_pages, void* v_pages, void* o, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/* The model's forward over a step planned by nc_page_plan: tokens [rows] packed
+ * (rows behind the last request's need a valid id), the new positions' k, v into
+ * every layer of kv_pages, and the softcapped logits of every request's last new
+ * token into logits [n_req, V] (weights' type; zeros for a request without new
+ * tokens).  workspace: nc_paged_workspace_bytes(m, n_req, rows) bytes. */
+size_t nc_paged_workspace_bytes(const nc_model* m, int n_req, int rows);
+int nc_paged_forward(nc_model* m, const int32_t* tokens, int rows, int n_req, int max_new, const int32_t* positions,
+                     const int32_t* cu_rows, const int32_t* kv_len, const int32_t* slots, const int32_t* block_table,
+                     int max_blocks, int page_size, int n_pages, const void* weights, void* kv_pages, void* logits,
+                     void* workspace, size_t ws_bytes, void* stream);
+
+/* Beam search's selection.  Every batch row has `beams` beams (1..32) with
+ * cumulative log-probabilities scores [batch, beams] (fp32) and next-token
+ * logits [batch * beams, V] in the weights' type, as nc_prefill, nc_decode_step
+ * and nc_paged_forward write them.  Candidate (k, v) has the score
+ *   scores[k] + logits[k][v] - logsumexp(logits[k]);
+ * a beam with finished[b, k] != 0 has one candidate, token eos at scores[k], and
+ * its logits are not read.  The `beams` best candidates of a batch row, best
+ * first, go to scores_out (fp32, rounded once), tokens and parents [batch,
+ * beams] (int32; a parent is a beam of the same batch row, 0..beams-1), and
+ * finished_out (the parent was finished, or the token is eos).  Within a beam
+ * candidates go by logit, then the lower id; between beams by score in 64 bits,
+ * then the lower beam.  NaN logits and scores count as -inf; a beam whose logits
+ * are all -inf, or hold +inf, has candidates of score -inf.
+ * finished and finished_out: both given with eos in [0, V), or both NULL (eos is
+ * then -1 and no beam ends).  The outputs may be the inputs' own buffers. */
+#define NC_MAX_BEAMS 32
+int nc_beam_select(nc_model* m, const void* logits, int batch, int beams, const float* scores,
+                   const int32_t* finished, int eos, float* scores_out, int32_t* tokens, int32_t* parents,
+                   int32_t* finished_out, void* stream);
+
+/* The cache follows the selection's back-pointers, in place and for every layer:
+ * positions start..end-1 of row b * beams + i become those of row
+ * b * beams + parents[b, i] (as they were before the call).  Positions that all
+ * beams of a row share, such as the prompt's, need not be moved.
+ *   nc_beam_reorder: the cache of nc_prefill / nc_decode_step with batch * beams
+ *     rows, one span for all of them.
+ *   nc_beam_reorder_paged: the paged cache and block table of batch * beams
+ *     requests; starts, ends: device int32 [batch * beams], each row's span.
+ *     Where a beam and its parent have the same page nothing moves; a page that
+ *     is written must belong to one row alone.
+ * A parent outside [0, beams) keeps its row as it is and is reported as
+ * NC_ERR_BAD_LENGTH; a position without a page is passed over and reported as
+ * NC_ERR_BAD_PAGE. */
+int nc_beam_reorder(nc_model* m, void* kv_cache, int batch, int beams, int T_max, const int32_t* parents, int start,
+                    int end, void* stream);
+int nc_beam_reorder_paged(nc_model* m, void* kv_pages, int batch, int beams, int n_pages, int page_size,
+                          const int32_t* parents, const int32_t* block_table, int max_blocks, const int32_t* starts,
+                          const int32_t* ends, void* stream);
 
 /* LM head strategy of nc_forward_backward (both never hold the full [B*T, V]
  * logit tensor; B*T rows are processed R at a time):
