@@ -750,7 +750,8 @@ int nc_paged_forward(nc_model* m, const int32_t* tokens, int rows, int n_req, in
                      int max_blocks, int page_size, int n_pages, const void* weights, void* kv_pages, void* logits,
                      void* workspace, size_t ws_bytes, void* stream) {
     const void* ptrs[] = {tokens, positions, cu_rows, kv_len, slots, block_table, weights, kv_pages, logits, workspace};
-    int v = check_paged_step(n_req, rows, max_new, max_blocks, page_size, n_pages);
+    if (!m) return NC_ERR_INVALID_ARG;
+    int v = check_paged_step(m, n_req, rows, max_new, max_blocks, page_size, n_pages);
     if (v != NC_OK) return v;
     v = validate_call(m, 1, rows, ws_bytes, ptrs, 10, true);
     if (v != NC_OK) return v;

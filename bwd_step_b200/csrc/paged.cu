@@ -300,9 +300,11 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restric
     __syncthreads();
     const int r = s_r;
     if (r < 0) return;  // a row behind the last sequence stays as it was
-    const int cap = min((long long)kv.max_blocks * kv.page, 0x7fffffffll);
-    const int len = min(kv.kv_len[r] - (kv.cu_rows[r + 1] - row) + 1, cap);  // keys that the row sees
-    if (threadIdx.x == 0 && h == 0 && (kv.kv_len[r] > cap || len <= 0)) set_status(status, ST_BAD_LENGTH);
+    const int len = kv.kv_len[r] - (kv.cu_rows[r + 1] - row) + 1;  // keys that the row sees
+    if (kv.kv_len[r] > (long long)kv.max_blocks * kv.page || len <= 0) {
+        if (threadIdx.x == 0 && h == 0) set_status(status, ST_BAD_LENGTH);
+        return;
+    }
     const int32_t* table = kv.table + (size_t)r * kv.max_blocks;
     const int shift = 31 - __clz(kv.page);
     const int g = h / (H / nkv);
@@ -318,10 +320,9 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restric
             if ((unsigned)page < (unsigned)kv.n_pages) slot = (page << shift) + (j & (kv.page - 1));
             else set_status(status, ST_BAD_PAGE);
         }
-        float sc = -INFINITY;
+        float sc = j < len ? 0.f : -INFINITY;  // a position without a page reads as zeros
         if (slot >= 0) {
             const A* kr = kc + (size_t)slot * ld + (size_t)g * HD;
-            sc = 0.f;
 #pragma unroll
             for (int c = 0; c < HD; c += VEC) {
                 float x[VEC];
@@ -523,15 +524,6 @@ cudaError_t launch_last_rows(DType at, const void* x, int d, int rows, const int
                                                       reinterpret_cast<float*>(out));
     count_launch();
     return cudaGetLastError();
-}
-
-size_t paged_attention_workspace(DType, int, int, int) { return 256; }
-
-cudaError_t paged_attention(DType at, const void* qkv, int H, int nkv, int hd, int rows, int, const int32_t* slots,
-                            const PagedKv& kv, void* o, void*, int* status, cudaStream_t s) {
-    cudaError_t e = launch_paged_append(at, qkv, H, nkv, hd, rows, slots, kv, status, s);
-    if (e != cudaSuccess) return e;
-    return launch_paged_attention_simt(at, qkv, H, nkv, hd, rows, kv, o, status, s);
 }
 
 cudaError_t launch_beam_reorder(const ReorderArgs& a, cudaStream_t s) {

@@ -3,6 +3,8 @@
 #pragma once
 #include "kernels.h"
 
+struct nc_model;
+
 namespace nc {
 
 // Requests that one plan or attention call takes: their prefix sums live in
@@ -47,7 +49,7 @@ cudaError_t paged_attention(DType at, const void* qkv, int H, int nkv, int hd, i
                             const int32_t* slots, const PagedKv& kv, void* o, void* workspace, int* status,
                             cudaStream_t s);
 // Sizes of a paged step that the kernels take (NC_OK or the error code).
-int check_paged_step(int n_req, int rows, int max_new, int max_blocks, int page_size, int n_pages);
+int check_paged_step(const nc_model* m, int n_req, int rows, int max_new, int max_blocks, int page_size, int n_pages);
 size_t paged_attention_workspace(DType at, int H, int nkv, int hd);
 
 // Rows (b, i) of a cache, i < beams, take the entries of row (b, parents[b, i]) at positions start..end-1, in place.

@@ -38,10 +38,13 @@ int done(cudaError_t e) { return e == cudaSuccess ? NC_OK : NC_ERR_CUDA; }
 }  // namespace
 
 namespace nc {
-int check_paged_step(int n_req, int rows, int max_new, int max_blocks, int page_size, int n_pages) {
+int check_paged_step(const nc_model* m, int n_req, int rows, int max_new, int max_blocks, int page_size, int n_pages) {
     if (max_new < 0) return NC_ERR_INVALID_ARG;
     const int r = check_paging(page_size, max_blocks, n_pages);
-    return r == NC_OK ? check_requests(n_req, rows, max_blocks) : r;
+    if (r != NC_OK) return r;
+    // the attention counts 64-key tiles of all requests and K/V heads in 31 bits
+    if ((long long)n_req * max_blocks * page_size / 64 > 0x7fffffffll / m->nkv - n_req) return NC_ERR_UNSUPPORTED_SHAPE;
+    return check_requests(n_req, rows, max_blocks);
 }
 }  // namespace nc
 
@@ -60,7 +63,7 @@ int nc_page_plan(nc_model* m, int n_req, int page_size, int max_blocks, int n_pa
     if (!all4({cached_len, new_len, block_table, free_pages, free_count, cu_rows, kv_len, positions, slots}) ||
         !al4(release))
         return NC_ERR_INVALID_ARG;
-    const int r = check_paged_step(n_req, rows, 0, max_blocks, page_size, n_pages);
+    const int r = check_paged_step(m, n_req, rows, 0, max_blocks, page_size, n_pages);
     if (r != NC_OK) return r;
     return done(launch_page_plan(n_req, page_size, max_blocks, n_pages, rows, cached_len, new_len, release,
                                  block_table, free_pages, free_count, cu_rows, kv_len, positions, slots, m->status,
@@ -81,7 +84,7 @@ int nc_paged_attention(nc_model* m, const void* qkv, int rows, int n_req, int ma
     if (!qkv || !k_pages || !v_pages || !o || !workspace || !al16(qkv) || !al16(k_pages) || !al16(v_pages) ||
         !al16(o) || (reinterpret_cast<uintptr_t>(workspace) & 255))
         return NC_ERR_INVALID_ARG;
-    const int r = check_paged_step(n_req, rows, max_new, max_blocks, page_size, n_pages);
+    const int r = check_paged_step(m, n_req, rows, max_new, max_blocks, page_size, n_pages);
     if (r != NC_OK) return r;
     if (ws_bytes < nc_paged_attention_workspace_bytes(m, n_req, rows)) return NC_ERR_WORKSPACE_TOO_SMALL;
     const PagedKv kv{k_pages, v_pages, block_table, cu_rows, kv_len, n_req, max_blocks, page_size, n_pages};

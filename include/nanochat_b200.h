@@ -231,7 +231,7 @@ int nc_decode_step(nc_model* m, const int32_t* tokens, int B, int pos, const voi
  * page_size: 16, 32, 64, 128 or 256.  block_table: device int32 [n_req,
  * max_blocks], -1 (or any value outside [0, n_pages)) where a block has no
  * page.  n_req <= 4096; max_blocks * page_size and n_pages * page_size at most
- * 2^30.  A position that a step writes must be in a page of its own: requests
+ * 2^30, n_req * n_kv_head * max_blocks * page_size about 2^37.  A position that a step writes must be in a page of its own: requests
  * may share a page only where none of them writes.
  *
  * nc_page_plan builds what a step of n_req requests needs from their lengths, on
@@ -275,7 +275,9 @@ int nc_page_plan(nc_model* m, int n_req, int page_size, int max_blocks, int n_pa
  *   o[i] = softmax(q K^T / sqrt(head_dim)) V into o [rows, n_head head_dim].
  *   Rows from cu_rows[n_req] on are left as they were.
  *   max_new: an upper bound of every request's number of new rows, 0 if none is
- *   known (it chooses the kernels, the results do not depend on it).
+ *   known (it chooses the kernels).  A request with more rows than that is
+ *   reported as NC_ERR_BAD_LENGTH and may be left without output, as is one whose
+ *   length or rows do not fit the table or the step.
  *   workspace: nc_paged_attention_workspace_bytes(m, n_req, rows) bytes,
  *   256-byte aligned; contents on entry are ignored.
  * A block without a page inside a request's length reads as zeros and is
