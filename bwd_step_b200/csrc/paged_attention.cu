@@ -1,19 +1,22 @@
-// Attention of a step's new tokens over the paged cache, bf16.
+// Attention of a step's new tokens over the paged cache, bf16, on the tensor cores.
 //
+// Chunks (two new tokens or more) run on tcgen05 in tiles of 128 rows, a row being a
+// (token, query head).  Bound by the tensor core and the exponentials.
 // Decoding requests (one new token): per K/V head the group's query heads, 16 at
 // most, are the rows of one small matrix product against every cached key, so
 // each key and value is read once for all of them.  Bound by HBM.
 //
 // Work is cut evenly over the SMs: the requests' key tiles of all K/V heads form
 // one line, and block c of G takes the tiles [c W / G, (c + 1) W / G) of its W.
-// A (request, K/V head) that lies in one block is finished there; one that is cut
-// leaves a partial output, row maximum and sum in each of its blocks, and a second
-// kernel joins them in the blocks' order, so the result does not depend on timing.
+// A unit (a (request, K/V head), or a part of a chunk) that lies in one block is finished
+// there; one that is cut leaves a partial output, row maximum and sum in each of its
+// blocks, and a last kernel joins them in the blocks' order, so the result does not depend on timing.
 // A block has at most two partial results: its first and its last piece.
 #include "paged.h"
 #include "tc_common.cuh"
 #include <cudaTypedefs.h>
 #include <algorithm>
+#include <type_traits>
 
 namespace nc {
 namespace {
@@ -24,14 +27,13 @@ constexpr int kDecRows = 16;     // query heads of a K/V head that the decode ke
 constexpr int kDecThreads = 288; // 8 consumer warps, then the producer
 constexpr float kLog2eF = 1.44269504088896340736f;
 
-// Rows of a partial result: halves of `half` rows, row i of a half is token i / Hg of
-// it and head i % Hg; `tokens` per half.  One int4 per block in `desc`, for the piece
-// that begins in this block and goes on in the next ones: first packed row, K/V head,
-// 2 * (number of blocks it lies in) + (its slot here), its tokens; z = 0: none.
+// Partial results of the G blocks, two pieces each.  `desc` tells of the unit that begins in a
+// block and goes on in the next ones: first packed row, K/V head, 2 * (blocks it lies in) + (its
+// piece's slot here; 0 in the others), tokens; z = 0: none.
 struct Partials {
-    float* o;      // [2 G, rows, HD] unnormalised
-    float2* ml;    // [2 G, rows] maximum (log2 domain), sum
-    int4* desc;    // [G]
+    float* o;    // [2 G, rows, HD] unnormalised
+    float2* ml;  // [2 G, rows] maximum (log2 domain), sum
+    int4* desc;  // [G]
 };
 
 struct DecodeArgs {
@@ -466,67 +468,579 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     pdl_wait();
 }
 
-// ---------------------------------------------------------------- joining the pieces
-// Block (c, y): rows of the output that begins in block c of the attention's grid and
-// goes on in the next ones; WPR warps to a row, each with every WPR-th piece.
-template <int HD, int WPR>
-__global__ void __launch_bounds__(256) paged_join_kernel(const Partials part, int half, int tokens, int H, int Hg,
-                                                         bf16* __restrict__ o) {
-    constexpr int E = HD / 32, RPB = 8 / WPR;
-    __shared__ float s_o[8][HD];
-    __shared__ float2 s_ml[8];
+// ---------------------------------------------------------------- chunks
+// A unit is 2 x `tt` new tokens of a request with the Hg query heads of one K/V head:
+// two halves of tt * Hg <= 128 rows (row i: token i / Hg, head i % Hg) that share the
+// unit's K and V tiles of 128 keys, so that a chunk fills the tensor core's 128 rows
+// whatever its length and K and V are read once for all heads.  The units' key tiles
+// form the line that is cut over the SMs.
+//   warp 0     TMA: Q of both halves (a [tt][Hg][64] box per 64 columns), then K_j and
+//              V_j into two rings, one copy per page piece and 64 columns, K one tile
+//              ahead of V; the lanes hold 32 pieces' slots and issue a copy each;
+//   warp 1     tcgen05.mma in the order ... O_a += P_a(j) V_j, S_a(j+1), O_b += P_b(j)
+//              V_j, S_b(j+1) ...: S = Q K^T into the half's 128 TMEM score columns,
+//              O += P V with P read from TMEM over the first half of them and V as an
+//              MN-major operand;
+//   warps 2-5  softmax of half a, warps 6-9 of half b: a row per thread, running maximum
+//              in the log2 domain that moves only when it grows by 2^8, P as packed bf16.
+// Bound by the softmax's exponentials and the products together, as the training
+// attention is.
+constexpr int kChunkThreads = 320;
+constexpr int kChunkRows = 256;
+constexpr int kPolyEvery = 8;  // one score in this many takes 2^x from the FMA pipe
+
+struct ChunkArgs {
+    PagedKv kv;
+    bf16* o;
+    Partials part;
+    int H, nkv, Hg, tt, rows, piece, max_new;  // piece: rows of one copy, min(page, 128)
+    bool skip_one;                             // requests with one new row are the decode kernel's
+    float scale_log2;
+    int* status;
+};
+
+template <int HD>
+struct ChunkLayout {
+    static constexpr int KB = HD / 64;
+    static constexpr int TILE = KB * 16384;  // [128 x HD] bf16, 128B-swizzled
+    static constexpr int KVSTG = HD == 128 ? 2 : 3;
+    static constexpr int K = 2 * TILE;
+    static constexpr int V = K + KVSTG * TILE;
+    static constexpr int BAR = V + KVSTG * TILE;
+    static constexpr int PRE = BAR + 256;
+    static constexpr int bytes(int n_req) { return PRE + (n_req + 1) * 8; }
+};
+static_assert(ChunkLayout<128>::bytes(kMaxRequests) + 1024 <= 232448, "chunk shared memory exceeds the per-block limit");
+
+// Key tiles of a request's chunk for one K/V head: over its units, the tiles up to each one's last token.
+__device__ __forceinline__ long long chunk_tiles(int n, int len, int unit) {
+    long long t = 0;
+    for (int e = min(n, unit);; e = min(n, e + unit)) {
+        t += (len - n + e + 127) >> 7;
+        if (e == n) return t;
+    }
+}
+
+// Walks the pieces of a block's part [x, x1) of the line; every role of the block walks alike.
+struct ChunkWalk {
+    long long x, x1, unit;     // unit: the current unit's first tile in the line
+    int r, g, b, row, n, len;  // request, K/V head, unit of the chunk; its first packed row, new rows, length
+    int tok0, toks, end, tiles, k0, k1;  // the unit's tokens [tok0, tok0 + toks), keys and tiles; the piece's tiles
+
+    __device__ __forceinline__ void set(const ChunkArgs& a) {
+        tok0 = b * 2 * a.tt;
+        toks = min(n - tok0, 2 * a.tt);
+        end = len - n + tok0 + toks;
+        tiles = (end + 127) >> 7;
+    }
+    __device__ __forceinline__ void start(const ChunkArgs& a, const long long* pre, long long from, long long to) {
+        x = from; x1 = to;
+        if (x >= x1) return;
+        r = find_request(pre, a.kv.n_req, x);
+        request(a.kv, a.rows, r, row, n, len);
+        const long long per = (pre[r + 1] - pre[r]) / a.nkv;
+        long long rem = x - pre[r];
+        g = (int)(rem / per);
+        rem -= g * per;
+        for (b = 0;; ++b) {
+            set(a);
+            if (rem < tiles) break;
+            rem -= tiles;
+        }
+        k0 = (int)rem;
+        unit = x - k0;
+        k1 = (int)min((long long)tiles, k0 + (x1 - x));
+    }
+    __device__ __forceinline__ void next(const ChunkArgs& a, const long long* pre) {
+        x += k1 - k0;
+        if (x >= x1) return;
+        if (tok0 + toks >= n) {
+            b = 0;
+            if (++g == a.nkv) {
+                g = 0;
+                do ++r;
+                while (pre[r + 1] == pre[r]);
+                request(a.kv, a.rows, r, row, n, len);
+            }
+        } else {
+            ++b;
+        }
+        set(a);
+        unit = x;
+        k0 = 0;
+        k1 = (int)min((long long)tiles, x1 - x);
+    }
+};
+
+// The three-input maximum.
+__device__ __forceinline__ float max3f(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Store 32 consecutive 32-bit columns of this thread's TMEM lane (no wait).
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// 2^x on the FMA pipe, as in the training attention: x = n + f, 2^f by a cubic fitted
+// on [-1/2, 1/2] (maximum relative error 7.5e-5, below the rounding of P to bf16).
+__device__ __forceinline__ float exp2_fma(float x) {
+    x = fmaxf(x, -126.f);
+    const float t = x + 12582912.f;
+    const float f = x - (t - 12582912.f);
+    float p = fmaf(0.0551716685f, f, 0.2426111251f);
+    p = fmaf(p, f, 0.6932609677f);
+    p = fmaf(p, f, 0.9999280572f);
+    return __int_as_float(__float_as_int(p) + (__float_as_int(t) << 23));
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const ChunkArgs a) {
+    using Lay = ChunkLayout<HD>;
+    constexpr int KB = Lay::KB, TILE = Lay::TILE, KVSTG = Lay::KVSTG;
+    extern __shared__ __align__(1024) uint8_t smem_dyn[];
+    if ((smem_u32(smem_dyn) & 1023u) != 0) {
+        if (threadIdx.x == 0) set_status(a.status, ST_BAD_LAYOUT);
+        return;
+    }
     pdl_trigger();
-    pdl_wait();
-    const int4 d = part.desc[blockIdx.x];
+    const uint32_t sQ = smem_u32(smem_dyn), sK = sQ + Lay::K, sV = sQ + Lay::V;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem_dyn + Lay::BAR);
+    const uint32_t b0 = smem_u32(bars);
+    const uint32_t q_full = b0, q_empty = b0 + 8;
+    const uint32_t k_full = b0 + 16, k_empty = k_full + 8 * KVSTG;
+    const uint32_t v_full = k_empty + 8 * KVSTG, v_empty = v_full + 8 * KVSTG;
+    const uint32_t s_full = v_empty + 8 * KVSTG;  // [2] per half
+    const uint32_t p_full = s_full + 16, o_full = p_full + 16;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8 + 4 * KVSTG);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    long long* pre = reinterpret_cast<long long*>(smem_dyn + Lay::PRE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int st = 0; st < KVSTG; ++st) {
+            mbar_init(k_full + 8 * st, 1); mbar_init(k_empty + 8 * st, 1);
+            mbar_init(v_full + 8 * st, 1); mbar_init(v_empty + 8 * st, 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(s_full + 8 * x, 1);
+            mbar_init(p_full + 8 * x, 4);
+            mbar_init(o_full + 8 * x, 1);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch(&tm_q);
+        tma_prefetch(&tm_k);
+        tma_prefetch(&tm_v);
+    }
+    block_prefix<kChunkThreads>(pre, a.kv.n_req, [&](int r) -> long long {
+        int lo, n, len;
+        const bool ok = request(a.kv, a.rows, r, lo, n, len);
+        if (blockIdx.x == 0 && (!ok || (a.max_new > 0 && n > a.max_new))) set_status(a.status, ST_BAD_LENGTH);
+        if (!ok || n == 0 || (a.skip_one && n == 1)) return 0;
+        return a.nkv * chunk_tiles(n, len, 2 * a.tt);
+    });
+    const long long W = pre[a.kv.n_req];
+    const int G = (int)max(1ll, min((long long)gridDim.x, W));
+    pdl_wait();  // the new keys and values are in their pages
+    if (W == 0 || (int)blockIdx.x >= G) {
+        if (threadIdx.x == 0) a.part.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    const long long x0 = cut(W, G, blockIdx.x), x1 = cut(W, G, blockIdx.x + 1);
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // TMEM: scores (then P) of halves a and b in columns [0, 128) and [128, 256), their
+    // outputs O in [256, 256 + HD) and [256 + HD, 256 + 2 HD)
+
+    ChunkWalk w;
+    w.start(a, pre, x0, x1);
+    if (warp == 0) {
+        const int pshift = 31 - __clz(a.piece), shift = 31 - __clz(a.kv.page);
+        const int per = 128 >> pshift;  // pieces of a tile
+        const int p = lane / KB, c = lane % KB;
+        const uint32_t bytes_q = (uint32_t)(a.tt * a.Hg) * HD * 2;
+        int k = 0, ki = 0, vi = 0, have, entry, k_row = 0, k_np = 0;
+        bool ok = true;
+        // the tile's first piece's slot of this lane, from the table entries kept in the lanes
+        auto load = [&](bool isv, int i, int row, int np) -> bool {
+            const int st = i % KVSTG;
+            const uint32_t full_b = (isv ? v_full : k_full) + 8 * st, empty_b = (isv ? v_empty : k_empty) + 8 * st;
+            if (!warp_wait(empty_b, ((i / KVSTG) & 1) ^ 1, abort_flag, a.status)) return false;
+            if (lane == 0) mbar_expect_tx(full_b, (uint32_t)(np << pshift) * HD * 2);
+            __syncwarp();
+            if (p < np)
+                tma_load_2d((isv ? sV : sK) + st * TILE + c * 16384 + (p << pshift) * 128, isv ? &tm_v : &tm_k,
+                            w.g * HD + 64 * c, row, full_b);
+            return true;
+        };
+        for (; ok && w.x < w.x1; w.next(a, pre), ++k) {
+            if (!warp_wait(q_empty, (k & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
+            const bool two = w.toks > a.tt;
+            if (lane == 0) {
+                mbar_expect_tx(q_full, two ? 2 * bytes_q : bytes_q);
+                for (int h = 0; h < (two ? 2 : 1); ++h)
+#pragma unroll
+                    for (int cc = 0; cc < KB; ++cc)
+                        tma_load_3d(sQ + h * TILE + cc * 16384, &tm_q, 64 * cc, w.g * a.Hg, w.row + w.tok0 + h * a.tt, q_full);
+            }
+            __syncwarp();
+            const int32_t* table = a.kv.table + (size_t)w.r * a.kv.max_blocks;
+            have = -1;
+            entry = 0;
+            auto fetch = [&](int kt) {  // the slots of tile kt's pieces: k_row of this lane, k_np pieces
+                const int p0 = kt * per;
+                k_np = min(per, (w.end - kt * 128 + a.piece - 1) >> pshift);
+                if (have < 0 || p0 + k_np > have + 32) {
+                    have = p0;
+                    const int pos = (p0 + lane) << pshift;
+                    entry = a.kv.n_pages << shift;  // past the end: reads as zeros
+                    if (pos < w.end) {
+                        const int page = table[pos >> shift];
+                        if ((unsigned)page < (unsigned)a.kv.n_pages) entry = (page << shift) + (pos & (a.kv.page - 1));
+                        else set_status(a.status, ST_BAD_PAGE);
+                    }
+                }
+                k_row = __shfl_sync(0xffffffffu, entry, p0 - have + p);
+            };
+            fetch(w.k0);
+            if (!load(false, ki++, k_row, k_np)) { ok = false; break; }
+            for (int kt = w.k0; kt < w.k1; ++kt) {
+                const int row = k_row, np = k_np;
+                if (kt + 1 < w.k1) {
+                    fetch(kt + 1);
+                    if (!load(false, ki++, k_row, k_np)) { ok = false; break; }
+                }
+                if (!load(true, vi++, row, np)) { ok = false; break; }
+            }
+        }
+        if (!ok && lane == 0) {  // copies in flight land before the block exits (1 ms each at most)
+            auto drain = [&](uint32_t bar, uint32_t parity) {
+                const uint64_t t0 = globaltimer();
+                while (!mbar_try(bar, parity) && globaltimer() - t0 < 1000000ull) {}
+            };
+            drain(q_full, k & 1);
+            for (int i = max(0, ki - KVSTG); i < ki; ++i) drain(k_full + 8 * (i % KVSTG), (i / KVSTG) & 1);
+            for (int i = max(0, vi - KVSTG); i < vi; ++i) drain(v_full + 8 * (i % KVSTG), (i / KVSTG) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t id_s = idesc_bf16(128, 128, false, false);
+            const uint32_t id_o = idesc_bf16(128, HD, false, true);
+            int k = 0, ki = 0, vi = 0;
+            uint32_t pcnt0 = 0, pcnt1 = 0;  // P hand-overs waited for, per half
+            bool ok = true;
+            auto ready = [&](bool isv, int i) -> bool {
+                return mbar_wait((isv ? v_full : k_full) + 8 * (i % KVSTG), (i / KVSTG) & 1, abort_flag, a.status);
+            };
+            auto scores = [&](int x, int st) {
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+                    mma_bf16(tmem + 128 * x, smem_desc(sQ + x * TILE + off, 16, 1024),
+                             smem_desc(sK + st * TILE + off, 16, 1024), id_s, ks > 0 ? 1u : 0u);
+                }
+                mma_commit(s_full + 8 * x);
+            };
+            // O_x += P_x V: keys 16kk..16kk+15 sit in the packed columns 8kk..8kk+7
+            auto pv = [&](int x, int st, bool acc) -> bool {
+                if (!mbar_wait(p_full + 8 * x, (x ? pcnt1 : pcnt0) & 1, abort_flag, a.status)) return false;
+                if (x) ++pcnt1;
+                else ++pcnt0;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_bf16_ts(tmem + 256 + x * HD, tmem + 128 * x + 8 * kk,
+                                smem_desc(sV + st * TILE + kk * 2048, 16384, 1024), id_o, (acc || kk > 0) ? 1u : 0u);
+                return true;
+            };
+            for (; ok && w.x < w.x1; w.next(a, pre), ++k) {
+                const bool two = w.toks > a.tt;
+                const int nblk = w.k1 - w.k0;
+                if (!mbar_wait(q_full, k & 1, abort_flag, a.status) || !ready(false, ki)) { ok = false; break; }
+                tc_fence_after();
+                scores(0, ki % KVSTG);
+                if (two) scores(1, ki % KVSTG);
+                mma_commit(k_empty + 8 * (ki % KVSTG));
+                ++ki;
+                if (nblk == 1) mma_commit(q_empty);  // the piece's last products that read Q
+                for (int j = 0; j < nblk; ++j) {
+                    const bool more = j + 1 < nblk;
+                    const int vst = vi % KVSTG;
+                    if (!ready(true, vi)) { ok = false; break; }
+                    // half a: O += P(j) V_j, then S(j+1) (which overwrites P(j) after it, in issue order)
+                    if (!pv(0, vst, j > 0)) { ok = false; break; }
+                    if (more) {
+                        if (!ready(false, ki)) { ok = false; break; }
+                        tc_fence_after();
+                        scores(0, ki % KVSTG);
+                    } else {
+                        mma_commit(o_full);
+                    }
+                    // half b likewise; V_j and (after both halves' scores) K_{j+1} are then released
+                    if (two && !pv(1, vst, j > 0)) { ok = false; break; }
+                    mma_commit(v_empty + 8 * vst);
+                    ++vi;
+                    if (more) {
+                        if (two) scores(1, ki % KVSTG);
+                        mma_commit(k_empty + 8 * (ki % KVSTG));
+                        ++ki;
+                    } else if (two) {
+                        mma_commit(o_full + 8);
+                    }
+                    if (j + 2 == nblk) mma_commit(q_empty);
+                }
+            }
+        }
+    } else {
+        // ---------------- softmax: half x, TMEM lane quarter q, one row per thread
+        const int x = (warp - 2) >> 2, q = warp & 3;
+        const int r = q * 32 + lane;
+        const int rt = r / a.Hg;  // token of the half
+        const bool in = r < a.tt * a.Hg;
+        const uint32_t lane_off = (uint32_t)(q * 32) << 16;
+        const uint32_t tS = tmem + lane_off + 128 * x, tO = tmem + lane_off + 256 + x * HD;
+        uint32_t scnt = 0, ocnt = 0;
+        int4 d = make_int4(0, 0, 0, 0);
+        for (; w.x < w.x1; w.next(a, pre)) {
+            if (w.unit >= x0 && w.unit + w.tiles > x1)
+                d = make_int4(w.row + w.tok0, w.g,
+                              2 * (block_of(W, G, w.unit + w.tiles - 1) - (int)blockIdx.x + 1) + (w.unit == x0 ? 0 : 1), w.toks);
+            if (x == 1 && w.toks <= a.tt) continue;
+            const bool live = in && x * a.tt + rt < w.toks;
+            const int first = w.len - w.n + w.tok0 + x * a.tt;  // position of the half's first token
+            const int pos = live ? first + rt : -1;             // the last key that the row sees
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int kt = w.k0; kt < w.k1; ++kt) {
+                if (!warp_wait(s_full + 8 * x, scnt & 1, abort_flag, a.status)) { ok = false; break; }
+                tc_fence_after();
+                const bool diag = kt * 128 + 127 > first;
+                const int lim = pos - kt * 128;  // key c of the tile is visible iff c <= lim
+                uint32_t sr[128];
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) tmem_ld32_issue(tS + 32 * q4, sr + 32 * q4);
+                if (x == 0 && kt == w.tiles - 1 && (w.end & 127)) {
+                    // the unit's last tile: values behind its keys are cleared (their weight is 0, but a page may
+                    // hold anything there).  V_j is released after P(j) V_j, so its barrier is in this tile's phase.
+                    const int st = scnt % KVSTG, v0 = w.end & 127;
+                    if (!warp_wait(v_full + 8 * st, (scnt / KVSTG) & 1, abort_flag, a.status)) ok = false;
+                    if (ok) {
+                        for (int i = v0 * 8 + (warp - 2) * 32 + lane; i < 128 * 8; i += 128)
+#pragma unroll
+                            for (int c = 0; c < KB; ++c)
+                                *reinterpret_cast<uint4*>(smem_dyn + Lay::V + st * TILE + c * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
+                }
+                ++scnt;
+                tmem_wait_ld();
+                if (!ok) break;
+                float mx4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx4[k] = -INFINITY;
+                if (diag) {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2)
+                        mx4[(c >> 1) & 3] = max3f(mx4[(c >> 1) & 3], c > lim ? -INFINITY : __uint_as_float(sr[c]),
+                                                  c + 1 > lim ? -INFINITY : __uint_as_float(sr[c + 1]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2)
+                        mx4[(c >> 1) & 3] = max3f(mx4[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                }
+                float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+                mx *= a.scale_log2;
+                const bool rescale = mx > m + 8.f;
+                const float mu = rescale ? mx : m;
+                const float alpha = rescale ? ex2(m - mx) : 1.f;
+                const float nmu = mu == -INFINITY ? 0.f : -mu;  // no key seen yet: every weight is 2^-inf = 0
+                const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nmu2 = f2_pack(nmu, nmu);
+                uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                auto exp_pack = [&](auto poly) {
+                    constexpr bool kPoly = decltype(poly)::value;
+#pragma unroll
+                    for (int q8 = 0; q8 < 8; ++q8) {
+                        uint32_t pk[8];
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) {
+                            const int cc = 16 * q8 + c;
+                            float y0, y1;
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, nmu2), y0, y1);
+                            if (!kPoly && diag) {
+                                if (cc > lim) y0 = -INFINITY;
+                                if (cc + 1 > lim) y1 = -INFINITY;
+                            }
+                            const float e0 = ex2(y0);
+                            const float e1 = (kPoly && (c / 2) % (kPolyEvery / 2) == kPolyEvery / 2 - 1) ? exp2_fma(y1) : ex2(y1);
+                            sum2[(c >> 1) & 1] = f2_add(sum2[(c >> 1) & 1], f2_pack(e0, e1));
+                            pk[c >> 1] = pack2(e0, e1);
+                        }
+                        tmem_st8_nowait(tS + 8 * q8, pk);
+                    }
+                };
+                if (!diag) exp_pack(std::true_type{});
+                else exp_pack(std::false_type{});
+                tmem_wait_st();
+                float s00, s01, s10, s11;
+                f2_unpack(sum2[0], s00, s01);
+                f2_unpack(sum2[1], s10, s11);
+                const float sum = (s00 + s01) + (s10 + s11);
+                if (kt > w.k0 && __any_sync(0xffffffffu, rescale)) {
+                    // O_x += P(j-1) V has completed (S(j) was issued after it and has landed);
+                    // O_x += P(j) V waits for this warp's hand-over below
+#pragma unroll 1
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32_issue(tO + c * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(tO + c * 32, o);
+                        tmem_wait_st();
+                    }
+                }
+                l = l * alpha + sum;
+                m = mu;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * x);
+            }
+            if (!ok || !warp_wait(o_full + 8 * x, ocnt & 1, abort_flag, a.status)) break;
+            ++ocnt;
+            tc_fence_after();
+            const bool whole = w.k0 == 0 && w.k1 == w.tiles;
+            if (whole) {
+                const float inv = 1.f / l;
+                bf16* orow = a.o + (size_t)(w.row + w.tok0 + (live ? x * a.tt + rt : 0)) * a.H * HD + (size_t)(w.g * a.Hg + r % a.Hg) * HD;
+#pragma unroll 1
+                for (int c = 0; c < HD / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tO + c * 32, o);
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<uint4*>(orow + c * 32 + 8 * i) =
+                                make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv), pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                           pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    }
+                }
+            } else {
+                const size_t at = (size_t)(2 * blockIdx.x + (w.x == x0 ? 0 : 1)) * kChunkRows + x * 128 + r;
+                float* to = a.part.o + at * HD;
+#pragma unroll 1
+                for (int c = 0; c < HD / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(tO + c * 32, o);
+                    if (live) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<float4*>(to + c * 32 + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+                if (live) a.part.ml[at] = make_float2(m, l);
+            }
+            // the next piece's first product overwrites O: it waits for this half's P, handed over after these reads
+        }
+        if (threadIdx.x == 64) a.part.desc[blockIdx.x] = *abort_flag ? make_int4(0, 0, 0, 0) : d;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- joining the pieces
+// How one attention kernel's partial results lie (see Partials): its rows per piece, in halves of
+// `half` rows and `tokens` tokens, and how many blocks along y join them.
+struct JoinSet {
+    Partials part;
+    int rows, half, tokens, blocks;
+};
+
+// Rows of the output that begins in block c of the attention's grid and goes on in the next
+// ones, one row after another: WPR warps to a row, each with every WPR-th piece.
+template <int HD, int WPR>
+__device__ __forceinline__ void join_rows(const JoinSet& s, int y, int H, int Hg, bf16* __restrict__ o, float (*s_o)[HD],
+                                          float2* s_ml) {
+    constexpr int E = HD / 32, RPB = 8 / WPR;
+    const int4 d = s.part.desc[blockIdx.x];
     const int n = d.z >> 1;
     if (n == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int i = blockIdx.y * RPB + warp / WPR, rows = half * (tokens * Hg <= half && half > kDecRows ? 2 : 1);
-    const int in = i % half, tok = (i / half) * tokens + in / Hg;
-    const bool live = i < rows && in < tokens * Hg && tok < d.w;
-    float acc[E], m = -INFINITY, l = 0.f;
+    for (int i0 = y * RPB; i0 < s.rows; i0 += s.blocks * RPB) {
+        const int i = i0 + warp / WPR, in = i % s.half, tok = (i / s.half) * s.tokens + in / Hg;
+        const bool live = in < s.tokens * Hg && tok < d.w;
+        float acc[E], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (live) {
-        for (int k = warp % WPR; k < n; k += WPR) {
-            const size_t at = (size_t)(2 * (blockIdx.x + k) + (k == 0 ? d.z & 1 : 0)) * rows + i;
-            const float2 ml = part.ml[at];
-            float v[E];
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        auto add = [&](float om, float ol, const float* v) {
+            const float M = fmaxf(m, om);
+            const float c0 = m == -INFINITY ? 0.f : ex2(m - M), c1 = om == -INFINITY ? 0.f : ex2(om - M);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 t = *reinterpret_cast<const float2*>(part.o + at * HD + lane * E + e);
-                v[e] = t.x; v[e + 1] = t.y;
+            for (int e = 0; e < E; ++e) acc[e] = acc[e] * c0 + v[e] * c1;
+            l = l * c0 + ol * c1;
+            m = M;
+        };
+        if (live) {
+#pragma unroll 2
+            for (int k = warp % WPR; k < n; k += WPR) {
+                const size_t at = (size_t)(2 * (blockIdx.x + k) + (k == 0 ? d.z & 1 : 0)) * s.rows + i;
+                const float2 ml = s.part.ml[at];
+                float v[E];
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 t = *reinterpret_cast<const float2*>(s.part.o + at * HD + lane * E + e);
+                    v[e] = t.x; v[e + 1] = t.y;
+                }
+                add(ml.x, ml.y, v);
             }
-            const float M = fmaxf(m, ml.x);
-            const float c0 = m == -INFINITY ? 0.f : ex2(m - M), c1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * c0 + (c1 > 0.f ? v[e] * c1 : 0.f);
-            l = l * c0 + ml.y * c1;
-            m = M;
         }
-    }
-    if (WPR > 1) {
+        if (WPR > 1) {
+            __syncthreads();
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
-        if (lane == 0) s_ml[warp] = make_float2(m, l);
-        __syncthreads();
-        if (warp % WPR != 0) return;
+            for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+            if (lane == 0) s_ml[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp % WPR != 0) continue;
 #pragma unroll
-        for (int k = 1; k < WPR; ++k) {
-            const float2 ml = s_ml[warp + k];
-            const float M = fmaxf(m, ml.x);
-            const float c0 = m == -INFINITY ? 0.f : ex2(m - M), c1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * c0 + s_o[warp + k][lane * E + e] * c1;
-            l = l * c0 + ml.y * c1;
-            m = M;
+            for (int k = 1; k < WPR; ++k) add(s_ml[warp + k].x, s_ml[warp + k].y, &s_o[warp + k][lane * E]);
         }
-    }
-    if (!live) return;
-    const float inv = 1.f / l;
-    bf16* to = o + (size_t)(d.x + tok) * H * HD + (size_t)(d.y * Hg + in % Hg) * HD + lane * E;
+        if (!live) continue;
+        const float inv = 1.f / l;
+        bf16* to = o + (size_t)(d.x + tok) * H * HD + (size_t)(d.y * Hg + in % Hg) * HD + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(to + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(to + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+    }
+}
+
+// Both attention kernels' pieces: blocks y < dec.blocks the decoding requests' (few rows, up to as
+// many pieces as there are SMs), the others the chunks' (up to 256 rows, seldom more than three pieces).
+template <int HD>
+__global__ void __launch_bounds__(256) paged_join_kernel(const JoinSet dec, const JoinSet chunk, int H, int Hg, bf16* __restrict__ o) {
+    __shared__ float s_o[8][HD];
+    __shared__ float2 s_ml[8];
+    pdl_wait();
+    if ((int)blockIdx.y < dec.blocks) join_rows<HD, 4>(dec, blockIdx.y, H, Hg, o, s_o, s_ml);
+    else join_rows<HD, 1>(chunk, blockIdx.y - dec.blocks, H, Hg, o, s_o, s_ml);
 }
 
 // ---------------------------------------------------------------- host
@@ -577,9 +1091,7 @@ cudaError_t launch_pdl(const void* func, dim3 grid, int threads, int smem, cudaS
     return e;
 }
 
-bool decode_takes(DType at, int H, int nkv, int hd, int max_new) {
-    return at == DT_BF16 && (hd == 64 || hd == 128) && H / nkv <= kDecRows && max_new == 1;
-}
+bool tensor_core_takes(DType at, int H, int nkv, int hd) { return at == DT_BF16 && (hd == 64 || hd == 128) && H / nkv <= 128; }
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t partial_bytes(int blocks, int rows, int hd) {
@@ -596,45 +1108,63 @@ Partials partials(char* ws, int blocks, int rows, int hd) {
 }
 
 template <int HD>
-cudaError_t decode(DecodeArgs a, void* ws, cudaStream_t s) {
-    using Lay = DecLayout<HD>;
-    cudaError_t e = ensure_smem_limit((const void*)paged_decode_kernel<HD>, Lay::bytes(kMaxRequests));
+cudaError_t attention(const bf16* qkv, int H, int nkv, int rows, int max_new, const int32_t* slots, const PagedKv& kv, bf16* o,
+                      char* ws, int* status, cudaStream_t s) {
+    const int Hg = H / nkv, G = device_sm_count();
+    const float scale_log2 = kLog2eF / sqrtf((float)HD);
+    const bool decodes = Hg <= kDecRows, chunks = !decodes || max_new != 1;
+    JoinSet jd{}, jc{};
+    cudaError_t e;
+    if (decodes) {
+        if ((e = ensure_smem_limit((const void*)paged_decode_kernel<HD>, DecLayout<HD>::bytes(kMaxRequests))) != cudaSuccess) return e;
+        jd = {partials(ws, G, kDecRows, HD), kDecRows, kDecRows, 1, (Hg + 1) / 2};
+        ws += partial_bytes(G, kDecRows, HD);
+        DecodeArgs a{qkv, slots, kv, o, jd.part, H, nkv, Hg, rows, std::min(kv.page, kTile), max_new, scale_log2, status};
+        CUtensorMap tk, tv;
+        if (!map_pool(&tk, kv.k, nkv, HD, kv, a.piece) || !map_pool(&tv, kv.v, nkv, HD, kv, a.piece)) return cudaErrorUnknown;
+        paged_decode_kernel<HD><<<G, kDecThreads, DecLayout<HD>::bytes(kv.n_req), s>>>(tk, tv, a);
+        count_launch();
+        e = cudaGetLastError();
+    } else {
+        e = launch_paged_append(DT_BF16, qkv, H, nkv, HD, rows, slots, kv, status, s);
+    }
     if (e != cudaSuccess) return e;
-    const int G = device_sm_count();
-    a.part = partials((char*)ws, G, kDecRows, HD);
-    a.piece = std::min(a.kv.page, kTile);
-    CUtensorMap tk, tv;
-    if (!map_pool(&tk, a.kv.k, a.nkv, HD, a.kv, a.piece) || !map_pool(&tv, a.kv.v, a.nkv, HD, a.kv, a.piece))
-        return cudaErrorUnknown;
-    paged_decode_kernel<HD><<<G, kDecThreads, Lay::bytes(a.kv.n_req), s>>>(tk, tv, a);
-    count_launch();
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    int half = kDecRows, tokens = 1;
-    void* args[] = {&a.part, &half, &tokens, &a.H, &a.Hg, &a.o};
-    return launch_pdl((const void*)paged_join_kernel<HD, 4>, dim3(G, (a.Hg + 1) / 2), 256, 0, s, args);
+    if (chunks) {
+        if ((e = ensure_smem_limit((const void*)paged_chunk_kernel<HD>, ChunkLayout<HD>::bytes(kMaxRequests))) != cudaSuccess) return e;
+        const int tt = 128 / Hg;
+        jc = {partials(ws, G, kChunkRows, HD), kChunkRows, 128, tt, 8};
+        ChunkArgs a{kv, o, jc.part, H, nkv, Hg, tt, rows, std::min(kv.page, 128), max_new, decodes, scale_log2, status};
+        CUtensorMap tq, tk, tv;
+        const cuuint64_t ld = (cuuint64_t)(H + 2 * nkv) * HD * 2;
+        const cuuint64_t dq[3] = {HD, (cuuint64_t)(H + 2 * nkv), (cuuint64_t)rows}, sq[2] = {HD * 2, ld};
+        const cuuint32_t bq[3] = {64, (cuuint32_t)Hg, (cuuint32_t)tt};
+        const cuuint64_t dk[2] = {(cuuint64_t)nkv * HD, (cuuint64_t)kv.n_pages * kv.page}, sk[1] = {(cuuint64_t)nkv * HD * 2};
+        const cuuint32_t bk[2] = {64, (cuuint32_t)a.piece};
+        if (!encode(&tq, qkv, 3, dq, sq, bq) || !encode(&tk, kv.k, 2, dk, sk, bk) || !encode(&tv, kv.v, 2, dk, sk, bk))
+            return cudaErrorUnknown;
+        void* args[] = {&tq, &tk, &tv, &a};
+        e = launch_pdl((const void*)paged_chunk_kernel<HD>, dim3(G), kChunkThreads, ChunkLayout<HD>::bytes(kv.n_req), s, args);
+        if (e != cudaSuccess) return e;
+    }
+    void* args[] = {&jd, &jc, &H, const_cast<int*>(&Hg), &o};
+    return launch_pdl((const void*)paged_join_kernel<HD>, dim3(G, jd.blocks + jc.blocks), 256, 0, s, args);
 }
 
 }  // namespace
 
 size_t paged_attention_workspace(DType at, int H, int nkv, int hd) {
-    if (!decode_takes(at, H, nkv, hd, 1)) return 256;
-    return partial_bytes(device_sm_count(), kDecRows, hd);
+    if (!tensor_core_takes(at, H, nkv, hd)) return 256;
+    const int G = device_sm_count();
+    return partial_bytes(G, kDecRows, hd) + partial_bytes(G, kChunkRows, hd);
 }
 
 cudaError_t paged_attention(DType at, const void* qkv, int H, int nkv, int hd, int rows, int max_new,
                             const int32_t* slots, const PagedKv& kv, void* o, void* workspace, int* status,
                             cudaStream_t s) {
-    if (decode_takes(at, H, nkv, hd, max_new)) {
-        DecodeArgs a{};
-        a.qkv = reinterpret_cast<const bf16*>(qkv);
-        a.slots = slots;
-        a.kv = kv;
-        a.o = reinterpret_cast<bf16*>(o);
-        a.H = H; a.nkv = nkv; a.Hg = H / nkv; a.rows = rows; a.max_new = max_new;
-        a.scale_log2 = kLog2eF / sqrtf((float)hd);
-        a.status = status;
-        return hd == 128 ? decode<128>(a, workspace, s) : decode<64>(a, workspace, s);
+    if (tensor_core_takes(at, H, nkv, hd)) {
+        auto f = hd == 128 ? attention<128> : attention<64>;
+        return f(reinterpret_cast<const bf16*>(qkv), H, nkv, rows, max_new, slots, kv, reinterpret_cast<bf16*>(o), (char*)workspace,
+                 status, s);
     }
     cudaError_t e = launch_paged_append(at, qkv, H, nkv, hd, rows, slots, kv, status, s);
     if (e != cudaSuccess) return e;
