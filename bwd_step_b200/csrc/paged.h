@@ -74,6 +74,6 @@ cudaError_t launch_beam_reorder(const ReorderArgs& a, cudaStream_t s);
 constexpr int kMaxBeams = 32;
 cudaError_t launch_beam_select(DType at, const void* logits, int batch, int beams, int V, const float* scores,
                                const int32_t* finished, int eos, float* scores_out, int32_t* tokens, int32_t* parents,
-                               int32_t* finished_out, cudaStream_t s);
+                               int32_t* finished_out, int* status, cudaStream_t s);
 
 }  // namespace nc

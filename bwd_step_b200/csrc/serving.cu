@@ -101,7 +101,7 @@ int nc_beam_select(nc_model* m, const void* logits, int batch, int beams, const 
     if (finished ? eos < 0 || eos >= m->V : eos != -1) return NC_ERR_INVALID_ARG;
     if (beams > NC_MAX_BEAMS || batch > (1 << 20)) return NC_ERR_UNSUPPORTED_SHAPE;
     return done(launch_beam_select(m->at, logits, batch, beams, m->V, scores, finished, eos, scores_out, tokens,
-                                   parents, finished_out, (cudaStream_t)stream));
+                                   parents, finished_out, m->status, (cudaStream_t)stream));
 }
 
 int nc_beam_reorder(nc_model* m, void* kv_cache, int batch, int beams, int T_max, const int32_t* parents, int start,
