@@ -48,23 +48,29 @@ def _ptr(t, dtype=None, name="tensor", on_device=True, device=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _addr(t, dtype, name, device):
-    """Address of a contiguous tensor of that dtype on that GPU (_ptr's checks,
-    for the calls of a serving loop, where the host's time counts)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    at = t.get_device()
-    if at != device:
-        where = "in device memory" if at < 0 else f"on the model's cuda:{device}, not cuda:{at}"
-        raise ValueError(f"{name} must be {where}")
-    return t.data_ptr()
+def _serving():
+    """The compiled binding of the serving calls (raises if it has not been built)."""
+    global _serving_module
+    if _serving_module is None:
+        import torch  # noqa: F401  (its libraries are the binding's)
+        try:
+            from . import _serving as module
+        except ImportError as e:
+            raise RuntimeError("bwd_step_b200: the serving binding is missing; build it with `python -m bwd_step_b200.build` "
+                               "(or __graft_entry__.build())") from e
+        _serving_module = module
+    return _serving_module
 
 
-def _shape(t, want, name):
-    if t.shape != want:
-        raise ValueError(f"{name} must be {list(want)}, got {list(t.shape)}")
+_serving_module = None
+
+
+def _stream_of(stream, device):
+    """_stream_handle of a GPU, without the stream object, which takes 3 us to make."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return getattr(stream, "cuda_stream", stream)
 
 
 def _check_extents(n_params, vocab, tokens, targets=None, weights=None, grads=None, loss=None, logits=None):
@@ -134,6 +140,14 @@ class Model:
             self.close()
         except Exception:
             pass
+
+    @property
+    def _handle(self):
+        return self._h.value if self._h else None
+
+    @property
+    def _bf16(self):
+        return self.precision == "bf16"
 
     @property
     def weight_dtype(self):
@@ -258,35 +272,11 @@ class Model:
         pages given back (release [R]) and taken (block_table [R, blocks],
         free_pages [pages], free_count [1], in place), row offsets cu_rows [R + 1],
         lengths kv_len [R], and positions and slots [rows] of the packed rows."""
-        import torch
-        n, i32, dev = new_len.numel(), torch.int32, self.device
-        for name, t, want in (("cached_len", cached_len, (n,)), ("new_len", new_len, (n,)), ("cu_rows", cu_rows, (n + 1,)),
-                              ("kv_len", kv_len, (n,)), ("free_count", free_count, (1,)), ("slots", slots, positions.shape)):
-            _shape(t, want, name)
-        if block_table.dim() != 2 or block_table.shape[0] != n or free_pages.dim() != 1 or positions.dim() != 1:
-            raise ValueError("block_table must be [requests, blocks], free_pages [pages], positions and slots [rows]")
-        if release is not None:
-            _shape(release, (n,), "release")
-        _ok(lib().nc_page_plan(
-            self._h, n, page_size, block_table.shape[1], free_pages.numel(), positions.numel(),
-            _addr(cached_len, i32, "cached_len", dev), _addr(new_len, i32, "new_len", dev),
-            None if release is None else _addr(release, i32, "release", dev),
-            _addr(block_table, i32, "block_table", dev), _addr(free_pages, i32, "free_pages", dev),
-            _addr(free_count, i32, "free_count", dev), _addr(cu_rows, i32, "cu_rows", dev),
-            _addr(kv_len, i32, "kv_len", dev), _addr(positions, i32, "positions", dev), _addr(slots, i32, "slots", dev),
-            _stream_handle(stream)), "nc_page_plan")
-
-    def _paged_tables(self, rows, cu_rows, kv_len, slots, block_table):
-        """Checked addresses of a planned step's arrays."""
-        import torch
-        n, i32, dev = kv_len.numel(), torch.int32, self.device
-        _shape(kv_len, (n,), "kv_len")
-        _shape(cu_rows, (n + 1,), "cu_rows")
-        _shape(slots, (rows,), "slots")
-        if block_table.dim() != 2 or block_table.shape[0] != n:
-            raise ValueError("block_table must be [requests, blocks]")
-        return (n, _addr(cu_rows, i32, "cu_rows", dev), _addr(kv_len, i32, "kv_len", dev),
-                _addr(slots, i32, "slots", dev), _addr(block_table, i32, "block_table", dev), block_table.shape[1])
+        code = _serving().page_plan(self._handle, self.device, page_size, cached_len, new_len, release, block_table,
+                                    free_pages, free_count, cu_rows, kv_len, positions, slots,
+                                    _stream_of(stream, self.device))
+        if code:
+            _ok(code, "nc_page_plan")
 
     def paged_attention(self, qkv, cu_rows, kv_len, slots, block_table, k_pages, v_pages, o, workspace, max_new=0,
                         stream=None):
@@ -294,43 +284,24 @@ class Model:
         k_pages / v_pages [pages, page_size, n_kv_head, head_dim], and o [rows,
         n_head head_dim] of the rows qkv [rows, (n_head + 2 n_kv_head) head_dim]
         over their requests' positions.  max_new bounds a request's new rows."""
-        import torch
-        c, t, dev = self.cfg, self.weight_dtype, self.device
-        rows = qkv.shape[0]
-        _shape(qkv, (rows, (c.n_head + 2 * c.n_kv_head) * c.head_dim), "qkv")
-        _shape(o, (rows, c.n_head * c.head_dim), "o")
-        if k_pages.dim() != 4 or k_pages.shape[2] != c.n_kv_head or k_pages.shape[3] != c.head_dim:
-            raise ValueError("k_pages must be [pages, page_size, n_kv_head, head_dim]")
-        _shape(v_pages, k_pages.shape, "v_pages")
-        n, cu, kl, sl, table, blocks = self._paged_tables(rows, cu_rows, kv_len, slots, block_table)
-        _ok(lib().nc_paged_attention(
-            self._h, _addr(qkv, t, "qkv", dev), rows, n, max_new, cu, kl, sl, table, blocks, k_pages.shape[1],
-            k_pages.shape[0], _addr(k_pages, t, "k_pages", dev), _addr(v_pages, t, "v_pages", dev), _addr(o, t, "o", dev),
-            _addr(workspace, workspace.dtype, "workspace", dev), workspace.numel() * workspace.element_size(),
-            _stream_handle(stream)), "nc_paged_attention")
+        c = self.cfg
+        code = _serving().paged_attention(self._handle, self.device, self._bf16, c.n_head, c.n_kv_head, c.head_dim, max_new,
+                                          cu_rows, kv_len, slots, block_table, qkv, k_pages, v_pages, o, workspace,
+                                          _stream_of(stream, self.device))
+        if code:
+            _ok(code, "nc_paged_attention")
 
     def paged_forward(self, tokens, positions, cu_rows, kv_len, slots, block_table, weights, kv_pages, logits, workspace,
                       max_new=0, stream=None):
         """The forward of a planned step over the paged cache kv_pages [n_layer, 2,
         pages, page_size, n_kv_head, head_dim]: packed tokens [rows], the logits of
         every request's last new token into logits [requests, V]."""
-        import torch
-        c, t, dev, i32 = self.cfg, self.weight_dtype, self.device, torch.int32
-        rows = tokens.numel()
-        _shape(tokens, (rows,), "tokens")
-        _shape(positions, (rows,), "positions")
-        if weights.numel() < self.num_params():
-            raise ValueError("weights shorter than the flat layout")
-        if kv_pages.dim() != 6 or kv_pages.shape[:2] != (c.n_layer, 2) or kv_pages.shape[4:] != (c.n_kv_head, c.head_dim):
-            raise ValueError("kv_pages must be [n_layer, 2, pages, page_size, n_kv_head, head_dim]")
-        n, cu, kl, sl, table, blocks = self._paged_tables(rows, cu_rows, kv_len, slots, block_table)
-        _shape(logits, (n, c.vocab), "logits")
-        _ok(lib().nc_paged_forward(
-            self._h, _addr(tokens, i32, "tokens", dev), rows, n, max_new, _addr(positions, i32, "positions", dev), cu, kl,
-            sl, table, blocks, kv_pages.shape[3], kv_pages.shape[2], _addr(weights, t, "weights", dev),
-            _addr(kv_pages, t, "kv_pages", dev), _addr(logits, t, "logits", dev),
-            _addr(workspace, workspace.dtype, "workspace", dev), workspace.numel() * workspace.element_size(),
-            _stream_handle(stream)), "nc_paged_forward")
+        c = self.cfg
+        code = _serving().paged_forward(self._handle, self.device, self._bf16, c.n_layer, c.n_kv_head, c.head_dim, c.vocab,
+                                        self.num_params(), max_new, cu_rows, kv_len, slots, block_table, tokens, positions,
+                                        weights, kv_pages, logits, workspace, _stream_of(stream, self.device))
+        if code:
+            _ok(code, "nc_paged_forward")
 
     def beam_select(self, logits, scores, scores_out, tokens, parents, eos=-1, finished=None, finished_out=None,
                     stream=None):
@@ -338,61 +309,31 @@ class Model:
         V]) and scores [batch, beams] the best candidates of every batch row into
         scores_out, tokens and parents [batch, beams], and finished_out where beams
         end at eos (finished, finished_out int32 [batch, beams])."""
-        import torch
-        dev, i32, f32, want = self.device, torch.int32, torch.float32, scores.shape
-        if len(want) != 2:
-            raise ValueError("scores must be [batch, beams]")
-        v = self.cfg.vocab
-        if logits.shape != (*want, v) and logits.shape != (want[0] * want[1], v):
-            raise ValueError(f"logits must be [batch, beams, {v}] or [batch * beams, {v}]")
-        _shape(scores_out, want, "scores_out")
-        _shape(tokens, want, "tokens")
-        _shape(parents, want, "parents")
-        if (finished is None) != (finished_out is None):
-            raise ValueError("finished and finished_out go together")
-        fin = fin_out = None
-        if finished is not None:
-            _shape(finished, want, "finished")
-            _shape(finished_out, want, "finished_out")
-            fin, fin_out = _addr(finished, i32, "finished", dev), _addr(finished_out, i32, "finished_out", dev)
-        _ok(lib().nc_beam_select(
-            self._h, _addr(logits, self.weight_dtype, "logits", dev), want[0], want[1], _addr(scores, f32, "scores", dev),
-            fin, eos, _addr(scores_out, f32, "scores_out", dev), _addr(tokens, i32, "tokens", dev),
-            _addr(parents, i32, "parents", dev), fin_out, _stream_handle(stream)), "nc_beam_select")
+        code = _serving().beam_select(self._handle, self.device, self._bf16, self.cfg.vocab, eos, logits, scores, finished,
+                                      scores_out, tokens, parents, finished_out, _stream_of(stream, self.device))
+        if code:
+            _ok(code, "nc_beam_select")
 
     def beam_reorder(self, kv_cache, T_max, parents, start, end, stream=None):
         """Positions start..end-1 of the dense cache of batch * beams rows follow the
         back-pointers parents [batch, beams] (int32), in place."""
-        import torch
-        if parents.dim() != 2:
-            raise ValueError("parents must be [batch, beams]")
-        b, k = parents.shape
-        if kv_cache.numel() * kv_cache.element_size() < self.kv_cache_bytes(b * k, T_max):
-            raise ValueError("kv_cache smaller than kv_cache_bytes(batch * beams, T_max)")
-        _ok(lib().nc_beam_reorder(self._h, _addr(kv_cache, kv_cache.dtype, "kv_cache", self.device), b, k, T_max,
-                                  _addr(parents, torch.int32, "parents", self.device), start, end,
-                                  _stream_handle(stream)), "nc_beam_reorder")
+        c = self.cfg
+        each = c.n_layer * 2 * c.n_kv_head * c.head_dim * (2 if self._bf16 else 4)
+        code = _serving().beam_reorder(self._handle, self.device, each, kv_cache, T_max, parents, start, end,
+                                       _stream_of(stream, self.device))
+        if code:
+            _ok(code, "nc_beam_reorder")
 
     def beam_reorder_paged(self, kv_pages, parents, block_table, starts, ends, stream=None):
         """Positions starts..ends-1 of every row of the paged cache kv_pages follow the
         back-pointers parents [batch, beams], in place; block_table [batch * beams,
         blocks], starts and ends [batch * beams] (all int32)."""
-        import torch
-        c, dev, i32 = self.cfg, self.device, torch.int32
-        if parents.dim() != 2:
-            raise ValueError("parents must be [batch, beams]")
-        b, k = parents.shape
-        if kv_pages.dim() != 6 or kv_pages.shape[:2] != (c.n_layer, 2) or kv_pages.shape[4:] != (c.n_kv_head, c.head_dim):
-            raise ValueError("kv_pages must be [n_layer, 2, pages, page_size, n_kv_head, head_dim]")
-        if block_table.dim() != 2 or block_table.shape[0] != b * k:
-            raise ValueError("block_table must be [batch * beams, blocks]")
-        _shape(starts, (b * k,), "starts")
-        _shape(ends, (b * k,), "ends")
-        _ok(lib().nc_beam_reorder_paged(
-            self._h, _addr(kv_pages, self.weight_dtype, "kv_pages", dev), b, k, kv_pages.shape[2], kv_pages.shape[3],
-            _addr(parents, i32, "parents", dev), _addr(block_table, i32, "block_table", dev), block_table.shape[1],
-            _addr(starts, i32, "starts", dev), _addr(ends, i32, "ends", dev), _stream_handle(stream)),
-            "nc_beam_reorder_paged")
+        c = self.cfg
+        code = _serving().beam_reorder_paged(self._handle, self.device, self._bf16, c.n_layer, c.n_kv_head, c.head_dim,
+                                             kv_pages, parents, block_table, starts, ends,
+                                             _stream_of(stream, self.device))
+        if code:
+            _ok(code, "nc_beam_reorder_paged")
 
     def set_recompute(self, mlp: bool):
         """Recompute the MLP's relu(u), relu(u)^2 in the backward instead of

@@ -1,5 +1,6 @@
 """Builds libnanochat_b200.so in-tree with nvcc for sm_100a.
 
+Also builds _serving.so, the Python binding of the serving calls, against it.
 Each csrc/*.cu is compiled to an object under _build/ (in parallel, only when
 it or a header changed), then all objects are linked into one shared library
 next to this file.  Usage: python -m bwd_step_b200.build [--force] [-v]
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnanochat_b200.so")
+SERVING = os.path.join(HERE, "_serving.so")  # Python binding of the serving calls
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -69,7 +71,29 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_serving(force, verbose)
     return LIB
+
+
+def _build_serving(force: bool, verbose: bool):
+    src = os.path.join(CSRC, "serving_py.cpp")
+    newest = max(os.path.getmtime(f) for f in [src] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if not force and os.path.exists(SERVING) and os.path.getmtime(SERVING) >= newest:
+        return
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-DUSE_CUDA", *[f"-I{d}" for d in inc], src, "-o", SERVING, f"-L{HERE}", "-lnanochat_b200", "-Wl,-rpath,$ORIGIN",
+           f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building {SERVING} failed:\n{r.stdout}\n{r.stderr}")
 
 
 if __name__ == "__main__":

@@ -2,6 +2,7 @@
 // function attributes and device properties.
 #include "kernels.h"
 
+#include <atomic>
 #include <mutex>
 #include <set>
 #include <utility>
@@ -25,10 +26,12 @@ cudaError_t ensure_smem_limit(const void* func, int bytes) {
 }
 
 int device_sm_count() {
+    static std::atomic<int> known[64];  // per device: asked once
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        return 148;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 

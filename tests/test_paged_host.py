@@ -6,7 +6,6 @@ import pytest
 
 import bwd_step_b200
 from bwd_step_b200 import Model, _lib
-from bwd_step_b200.api import _addr, _shape
 from bwd_step_b200.generate import beam_search
 
 torch = pytest.importorskip("torch")
@@ -40,15 +39,20 @@ def test_the_library_refuses_a_null_model():
 
 
 def test_addresses_are_checked():
-    t = torch.zeros(8, dtype=torch.int32)
+    m = _model()
+    z, s, i = torch.zeros(2, 3, 512, dtype=torch.bfloat16), torch.zeros(2, 3), torch.zeros(2, 3, dtype=torch.int32)
     with pytest.raises(ValueError, match="device memory"):
-        _addr(t, torch.int32, "slots", 0)
-    with pytest.raises(TypeError):
-        _addr(t, torch.float32, "slots", 0)
+        m.beam_select(z, s, s, i, i, stream=0)
+    with pytest.raises(TypeError, match="expected torch.bfloat16, got torch.float32"):
+        m.beam_select(z.float(), s, s, i, i, stream=0)
     with pytest.raises(ValueError, match="contiguous"):
-        _addr(t[::2], torch.int32, "slots", 0)
-    with pytest.raises(ValueError):
-        _shape(t, (9,), "slots")
+        m.beam_select(torch.zeros(2, 512, 3, dtype=torch.bfloat16).transpose(1, 2), s, s, i, i, stream=0)
+    with pytest.raises(TypeError, match="must be a tensor"):
+        m.beam_select(z, s, s, [0], i, stream=0)
+    with pytest.raises(ValueError, match="eos is out of range"):
+        m.beam_select(z, s, s, i, i, eos=1 << 40, stream=0)
+    with pytest.raises(ValueError, match=r"tokens must be \[2, 3\], got \[6\]"):
+        m.beam_select(z, s, s, i.view(-1), i, stream=0)
 
 
 def test_shapes_are_checked_before_addresses():
@@ -56,25 +60,25 @@ def test_shapes_are_checked_before_addresses():
     i = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
     h = lambda *n: torch.zeros(*n, dtype=torch.bfloat16)  # noqa: E731
     with pytest.raises(ValueError, match="cu_rows"):
-        m.page_plan(16, i(2), i(2), i(2, 1), i(8), i(1), i(2), i(2), i(4), i(4))
+        m.page_plan(16, i(2), i(2), i(2, 1), i(8), i(1), i(2), i(2), i(4), i(4), stream=0)
     with pytest.raises(ValueError, match="block_table"):
-        m.page_plan(16, i(2), i(2), i(3, 1), i(8), i(1), i(3), i(2), i(4), i(4))
+        m.page_plan(16, i(2), i(2), i(3, 1), i(8), i(1), i(3), i(2), i(4), i(4), stream=0)
     with pytest.raises(ValueError, match="release"):
-        m.page_plan(16, i(2), i(2), i(2, 1), i(8), i(1), i(3), i(2), i(4), i(4), release=i(3))
+        m.page_plan(16, i(2), i(2), i(2, 1), i(8), i(1), i(3), i(2), i(4), i(4), release=i(3), stream=0)
     args = dict(qkv=h(4, 384), cu_rows=i(3), kv_len=i(2), slots=i(4), block_table=i(2, 5), k_pages=h(9, 16, 1, 64),
                 v_pages=h(9, 16, 1, 64), o=h(4, 256), workspace=torch.zeros(256, dtype=torch.uint8))
     for name, bad in (("qkv", h(4, 383)), ("cu_rows", i(2)), ("slots", i(5)), ("block_table", i(3, 5)), ("o", h(3, 256)),
                       ("k_pages", h(9, 16, 2, 64)), ("v_pages", h(8, 16, 1, 64))):
         with pytest.raises(ValueError, match=name):
-            m.paged_attention(**{**args, name: bad})
+            m.paged_attention(**{**args, name: bad}, stream=0)
     with pytest.raises(ValueError, match="logits"):
-        m.beam_select(h(2, 3, 511), torch.zeros(2, 3), torch.zeros(2, 3), i(2, 3), i(2, 3))
+        m.beam_select(h(2, 3, 511), torch.zeros(2, 3), torch.zeros(2, 3), i(2, 3), i(2, 3), stream=0)
     with pytest.raises(ValueError, match="together"):
-        m.beam_select(h(2, 3, 512), torch.zeros(2, 3), torch.zeros(2, 3), i(2, 3), i(2, 3), finished=i(2, 3))
+        m.beam_select(h(2, 3, 512), torch.zeros(2, 3), torch.zeros(2, 3), i(2, 3), i(2, 3), finished=i(2, 3), stream=0)
     with pytest.raises(ValueError, match="parents"):
-        m.beam_reorder_paged(h(2, 2, 9, 16, 1, 64), i(4), i(4, 5), i(4), i(4))
+        m.beam_reorder_paged(h(2, 2, 9, 16, 1, 64), i(4), i(4, 5), i(4), i(4), stream=0)
     with pytest.raises(ValueError, match="block_table"):
-        m.beam_reorder_paged(h(2, 2, 9, 16, 1, 64), i(2, 2), i(3, 5), i(4), i(4))
+        m.beam_reorder_paged(h(2, 2, 9, 16, 1, 64), i(2, 2), i(3, 5), i(4), i(4), stream=0)
 
 
 def test_searches_that_cannot_run_are_refused():
