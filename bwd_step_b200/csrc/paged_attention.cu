@@ -474,20 +474,20 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 // unit's K and V tiles of 128 keys, so that a chunk fills the tensor core's 128 rows
 // whatever its length and K and V are read once for all heads.  The units' key tiles
 // form the line that is cut over the SMs.
-//   warp 0     TMA: Q of both halves (a [tt][Hg][64] box per 64 columns), then K_j and
+//   warp 8     TMA: Q of both halves (a [tt][Hg][64] box per 64 columns), then K_j and
 //              V_j into two rings, one copy per page piece and 64 columns, K one tile
 //              ahead of V; the lanes hold 32 pieces' slots and issue a copy each;
-//   warp 1     tcgen05.mma in the order ... O_a += P_a(j) V_j, S_a(j+1), O_b += P_b(j)
+//   warp 9     tcgen05.mma in the order ... O_a += P_a(j) V_j, S_a(j+1), O_b += P_b(j)
 //              V_j, S_b(j+1) ...: S = Q K^T into the half's 128 TMEM score columns,
 //              O += P V with P read from TMEM over the first half of them and V as an
 //              MN-major operand;
-//   warps 2-5  softmax of half a, warps 6-9 of half b: a row per thread, running maximum
+//   warps 0-3  softmax of half a, warps 4-7 of half b: a row per thread, running maximum
 //              in the log2 domain that moves only when it grows by 2^8, P as packed bf16.
 // Bound by the softmax's exponentials and the products together, as the training
 // attention is.
-constexpr int kChunkThreads = 320;
+constexpr int kChunkThreads = 320;  // softmax of half a, of half b (a warpgroup each); producer, MMA, two idle warps
 constexpr int kChunkRows = 256;
-constexpr int kPolyEvery = 8;  // one score in this many takes 2^x from the FMA pipe
+constexpr int kPolyPairs = 1;  // pairs of scores, of every eight, that take 2^x from the FMA pipe
 
 struct ChunkArgs {
     PagedKv kv;
@@ -497,7 +497,16 @@ struct ChunkArgs {
     bool skip_one;                             // requests with one new row are the decode kernel's
     float scale_log2;
     int* status;
+
+    // Whether request r is this kernel's, and its first row, new rows and length.
+    __device__ __forceinline__ bool takes(int r, int& row, int& n, int& len) const {
+        return request(kv, rows, r, row, n, len) && n > (skip_one ? 1 : 0);
+    }
+    // Key tiles of request r over all K/V heads.
+    __device__ __forceinline__ long long tiles(int r) const;
 };
+
+constexpr int kGroup = 16;  // requests that one entry of the chunk kernel's prefix sums stands for
 
 template <int HD>
 struct ChunkLayout {
@@ -507,18 +516,43 @@ struct ChunkLayout {
     static constexpr int K = 2 * TILE;
     static constexpr int V = K + KVSTG * TILE;
     static constexpr int BAR = V + KVSTG * TILE;
-    static constexpr int PRE = BAR + 256;
-    static constexpr int bytes(int n_req) { return PRE + (n_req + 1) * 8; }
+    static constexpr int OUT = BAR + 256;         // 4 KB a softmax warp: its output's way to whole lines
+    static constexpr int PRE = OUT + 8 * 4096;    // [groups of requests + 1]
+    static constexpr int bytes(int n_req) { return PRE + ((n_req + kGroup - 1) / kGroup + 1) * 8; }
 };
-static_assert(ChunkLayout<128>::bytes(kMaxRequests) + 1024 <= 232448, "chunk shared memory exceeds the per-block limit");
+static_assert(ChunkLayout<128>::bytes(kMaxRequests) <= 232448, "chunk shared memory exceeds the per-block limit");
 
-// Key tiles of a request's chunk for one K/V head: over its units, the tiles up to each one's last token.
-__device__ __forceinline__ long long chunk_tiles(int n, int len, int unit) {
-    long long t = 0;
-    for (int e = min(n, unit);; e = min(n, e + unit)) {
-        t += (len - n + e + 127) >> 7;
-        if (e == n) return t;
+// sum of floor((a i + b) / 128) over i < n, for a <= 256: the whole parts are taken out, then what
+// is left counts the lattice points under a line, whose axes are exchanged until none is.
+__device__ __forceinline__ long long floor_sum128(unsigned n, unsigned a, unsigned b) {
+    long long sum = (long long)n * (b >> 7);
+    unsigned m = 128;
+    b &= 127;
+    while (n) {
+        if (a >= m) { sum += (long long)n * (n - 1) / 2 * (a / m); a %= m; }
+        if (b >= m) { sum += (long long)n * (b / m); b %= m; }
+        const unsigned y = a * n + b;  // a < 128, n < 2^24: below 2^31
+        n = y / m;
+        b = y % m;
+        const unsigned t = m;
+        m = a;
+        a = t;
     }
+    return sum;
+}
+
+// Key tiles of the first b units of a request's chunk for one K/V head: the tiles up to each unit's last token.
+__device__ __forceinline__ long long unit_tiles(int n, int len, int unit, int b) {
+    const int full = min(b, (n - 1) / unit);  // all but the chunk's last unit end `unit` tokens further on
+    long long t = full > 0 ? floor_sum128(full, unit, len - n + unit + 127) : 0;
+    if (b > full) t += (len + 127) >> 7;
+    return t;
+}
+__device__ __forceinline__ long long chunk_tiles(int n, int len, int unit) { return unit_tiles(n, len, unit, (n + unit - 1) / unit); }
+
+__device__ __forceinline__ long long ChunkArgs::tiles(int r) const {
+    int row, n, len;
+    return r < kv.n_req && takes(r, row, n, len) ? nkv * chunk_tiles(n, len, 2 * tt) : 0;
 }
 
 // Walks the pieces of a block's part [x, x1) of the line; every role of the block walks alike.
@@ -533,34 +567,53 @@ struct ChunkWalk {
         end = len - n + tok0 + toks;
         tiles = (end + 127) >> 7;
     }
+    // Out of line, so that the walk's state waits in local memory while a piece is worked on.
+    // By whole warps: the lanes look at a group's requests, then at 32 units, at once.
     __device__ __forceinline__ void start(const ChunkArgs& a, const long long* pre, long long from, long long to) {
         x = from; x1 = to;
         if (x >= x1) return;
-        r = find_request(pre, a.kv.n_req, x);
+        const int lane = threadIdx.x & 31, groups = (a.kv.n_req + kGroup - 1) / kGroup;
+        const int gr = find_request(pre, groups, x);
+        const long long mine = lane < kGroup ? a.tiles(gr * kGroup + lane) : 0;
+        long long before = mine;
+#pragma unroll
+        for (int o = 1; o < kGroup; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
+        }
+        before += pre[gr] - mine;
+        const unsigned in = __ballot_sync(0xffffffffu, lane < kGroup && before <= x && x < before + mine);
+        const int at = __ffs(in) - 1;
+        r = gr * kGroup + at;
+        long long rem = x - __shfl_sync(0xffffffffu, before, at);
+        const long long per = __shfl_sync(0xffffffffu, mine, at) / a.nkv;
         request(a.kv, a.rows, r, row, n, len);
-        const long long per = (pre[r + 1] - pre[r]) / a.nkv;
-        long long rem = x - pre[r];
         g = (int)(rem / per);
         rem -= g * per;
-        for (b = 0;; ++b) {
-            set(a);
-            if (rem < tiles) break;
-            rem -= tiles;
+        // the last unit that begins no later: 32 ways at a time
+        int lo = 0, hi = (n + 2 * a.tt - 1) / (2 * a.tt);  // tiles before unit lo <= rem < those before hi
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, b1 = min(hi, lo + lane * step);
+            const unsigned ok = __ballot_sync(0xffffffffu, b1 < hi && unit_tiles(n, len, 2 * a.tt, b1) <= rem);
+            const int k = 31 - __clz(ok);  // lane 0's is always
+            hi = min(hi, lo + (k + 1) * step);
+            lo += k * step;
         }
+        b = lo;
+        rem -= unit_tiles(n, len, 2 * a.tt, b);
+        set(a);
         k0 = (int)rem;
         unit = x - k0;
         k1 = (int)min((long long)tiles, k0 + (x1 - x));
     }
-    __device__ __forceinline__ void next(const ChunkArgs& a, const long long* pre) {
+    __device__ __forceinline__ void next(const ChunkArgs& a) {
         x += k1 - k0;
         if (x >= x1) return;
         if (tok0 + toks >= n) {
             b = 0;
             if (++g == a.nkv) {
                 g = 0;
-                do ++r;
-                while (pre[r + 1] == pre[r]);
-                request(a.kv, a.rows, r, row, n, len);
+                while (!a.takes(++r, row, n, len)) {}
             }
         } else {
             ++b;
@@ -579,29 +632,61 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
     return d;
 }
 
-// Store 32 consecutive 32-bit columns of this thread's TMEM lane (no wait).
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
-        "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
-        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
+// 8 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
+    tmem_wait_ld();
 }
 
-// 2^x on the FMA pipe, as in the training attention: x = n + f, 2^f by a cubic fitted
-// on [-1/2, 1/2] (maximum relative error 7.5e-5, below the rounding of P to bf16).
-__device__ __forceinline__ float exp2_fma(float x) {
-    x = fmaxf(x, -126.f);
-    const float t = x + 12582912.f;
-    const float f = x - (t - 12582912.f);
-    float p = fmaf(0.0551716685f, f, 0.2426111251f);
-    p = fmaf(p, f, 0.6932609677f);
-    p = fmaf(p, f, 0.9999280572f);
-    return __int_as_float(__float_as_int(p) + (__float_as_int(t) << 23));
+// 2^x of two values on the FMA pipe, as in the training attention: x = n + f, 2^f by a cubic
+// fitted on [-1/2, 1/2] (maximum relative error 7.5e-5, below the rounding of P to bf16), n
+// added to the exponent field.
+__device__ __forceinline__ void exp2_fma(uint64_t x, float& e0, float& e1) {
+    const uint64_t shift = f2_pack(12582912.f, 12582912.f), back = f2_pack(-12582912.f, -12582912.f);
+    float x0, x1, t0, t1, p0, p1;
+    f2_unpack(x, x0, x1);
+    x = f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+    const uint64_t t = f2_add(x, shift), n = f2_add(t, back);
+    const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), x);
+    uint64_t p = f2_fma(f2_pack(0.0551716685f, 0.0551716685f), f, f2_pack(0.2426111251f, 0.2426111251f));
+    p = f2_fma(p, f, f2_pack(0.6932609677f, 0.6932609677f));
+    p = f2_fma(p, f, f2_pack(0.9999280572f, 0.9999280572f));
+    f2_unpack(t, t0, t1);
+    f2_unpack(p, p0, p1);
+    e0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+    e1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+
+// The one thread of the warp that issues its products.  Chosen by elect.sync, not by its lane, so that
+// the compiler knows them to be uniform: beside busy warps a group of eight takes 520 cycles (the tensor
+// core's own time) where a branch on the lane takes 960.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+// D = A B^T over four K-steps of 16 (64 columns of the tiles), the descriptors 32 bytes apart.
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        " add.u64 x, %1, 2;\n add.u64 y, %2, 2;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+        " add.u64 x, %1, 4;\n add.u64 y, %2, 4;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n"
+        " add.u64 x, %1, 6;\n add.u64 y, %2, 6;\n tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, q;\n}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D += A B over four K-steps of 16 keys: A in TMEM, 8 columns apart, B MN-major, 2048 bytes apart.
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b32 x;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        " add.u32 x, %1, 8;\n add.u64 y, %2, 128;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n"
+        " add.u32 x, %1, 16;\n add.u64 y, %2, 256;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n"
+        " add.u32 x, %1, 24;\n add.u64 y, %2, 384;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, q;\n}\n"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 template <int HD>
@@ -623,8 +708,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const uint32_t k_full = b0 + 16, k_empty = k_full + 8 * KVSTG;
     const uint32_t v_full = k_empty + 8 * KVSTG, v_empty = v_full + 8 * KVSTG;
     const uint32_t s_full = v_empty + 8 * KVSTG;  // [2] per half
-    const uint32_t p_full = s_full + 16, o_full = p_full + 16;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8 + 4 * KVSTG);
+    const uint32_t p_full = s_full + 16, o_full = p_full + 32;  // [2][2] per half, its keys 0-63 and 64-127; [2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10 + 4 * KVSTG);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     long long* pre = reinterpret_cast<long long*>(smem_dyn + Lay::PRE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -637,7 +722,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(s_full + 8 * x, 1);
-            mbar_init(p_full + 8 * x, 4);
+            mbar_init(p_full + 16 * x, 4);
+            mbar_init(p_full + 16 * x + 8, 4);
             mbar_init(o_full + 8 * x, 1);
         }
         *abort_flag = 0;
@@ -646,14 +732,36 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tma_prefetch(&tm_k);
         tma_prefetch(&tm_v);
     }
-    block_prefix<kChunkThreads>(pre, a.kv.n_req, [&](int r) -> long long {
-        int lo, n, len;
-        const bool ok = request(a.kv, a.rows, r, lo, n, len);
-        if (blockIdx.x == 0 && (!ok || (a.max_new > 0 && n > a.max_new))) set_status(a.status, ST_BAD_LENGTH);
-        if (!ok || n == 0 || (a.skip_one && n == 1)) return 0;
-        return a.nkv * chunk_tiles(n, len, 2 * a.tt);
-    });
-    const long long W = pre[a.kv.n_req];
+    const int groups = (a.kv.n_req + kGroup - 1) / kGroup;
+    for (int base = 0; base < groups * kGroup; base += kChunkThreads) {
+        const int r = base + (int)threadIdx.x;
+        long long t = a.tiles(r);
+        if (blockIdx.x == 0 && r < a.kv.n_req) {
+            int lo, n, len;
+            if (!request(a.kv, a.rows, r, lo, n, len) || (a.max_new > 0 && n > a.max_new)) set_status(a.status, ST_BAD_LENGTH);
+        }
+#pragma unroll
+        for (int o = kGroup / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (r % kGroup == 0 && r / kGroup < groups) pre[r / kGroup] = t;
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive prefix sums, 32 groups at a time
+        long long run = 0;
+        for (int base = 0; base < groups; base += 32) {
+            const long long v = base + lane < groups ? pre[base + lane] : 0;
+            long long t = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, t, o);
+                if (lane >= o) t += y;
+            }
+            if (base + lane < groups) pre[base + lane] = run + t - v;
+            run += __shfl_sync(0xffffffffu, t, 31);
+        }
+        if (lane == 0) pre[groups] = run;
+    }
+    __syncthreads();
+    const long long W = pre[groups];
     const int G = (int)max(1ll, min((long long)gridDim.x, W));
     pdl_wait();  // the new keys and values are in their pages
     if (W == 0 || (int)blockIdx.x >= G) {
@@ -661,7 +769,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         return;
     }
     const long long x0 = cut(W, G, blockIdx.x), x1 = cut(W, G, blockIdx.x + 1);
-    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+    if (warp == 9) tmem_alloc(smem_u32(tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -671,7 +779,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     ChunkWalk w;
     w.start(a, pre, x0, x1);
-    if (warp == 0) {
+    if (warp == 8) {
         const int pshift = 31 - __clz(a.piece), shift = 31 - __clz(a.kv.page);
         const int per = 128 >> pshift;  // pieces of a tile
         const int p = lane / KB, c = lane % KB;
@@ -690,7 +798,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             w.g * HD + 64 * c, row, full_b);
             return true;
         };
-        for (; ok && w.x < w.x1; w.next(a, pre), ++k) {
+        for (; ok && w.x < w.x1; w.next(a), ++k) {
             if (!warp_wait(q_empty, (k & 1) ^ 1, abort_flag, a.status)) { ok = false; break; }
             const bool two = w.toks > a.tt;
             if (lane == 0) {
@@ -739,8 +847,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int i = max(0, ki - KVSTG); i < ki; ++i) drain(k_full + 8 * (i % KVSTG), (i / KVSTG) & 1);
             for (int i = max(0, vi - KVSTG); i < vi; ++i) drain(v_full + 8 * (i % KVSTG), (i / KVSTG) & 1);
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
+    } else if (warp == 9) {
+        if (elect_one()) {
             const uint32_t id_s = idesc_bf16(128, 128, false, false);
             const uint32_t id_o = idesc_bf16(128, HD, false, true);
             int k = 0, ki = 0, vi = 0;
@@ -750,27 +858,24 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 return mbar_wait((isv ? v_full : k_full) + 8 * (i % KVSTG), (i / KVSTG) & 1, abort_flag, a.status);
             };
             auto scores = [&](int x, int st) {
+                const uint64_t dq = smem_desc(sQ + x * TILE, 16, 1024), dk = smem_desc(sK + st * TILE, 16, 1024);
 #pragma unroll
-                for (int ks = 0; ks < HD / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-                    mma_bf16(tmem + 128 * x, smem_desc(sQ + x * TILE + off, 16, 1024),
-                             smem_desc(sK + st * TILE + off, 16, 1024), id_s, ks > 0 ? 1u : 0u);
-                }
+                for (int c = 0; c < KB; ++c) mma4(tmem + 128 * x, dq + c * 1024, dk + c * 1024, id_s, c > 0 ? 1u : 0u);
                 mma_commit(s_full + 8 * x);
             };
             // O_x += P_x V: keys 16kk..16kk+15 sit in the packed columns 8kk..8kk+7
             auto pv = [&](int x, int st, bool acc) -> bool {
-                if (!mbar_wait(p_full + 8 * x, (x ? pcnt1 : pcnt0) & 1, abort_flag, a.status)) return false;
-                if (x) ++pcnt1;
-                else ++pcnt0;
-                tc_fence_after();
+                const uint32_t par = (x ? pcnt1++ : pcnt0++) & 1;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ts(tmem + 256 + x * HD, tmem + 128 * x + 8 * kk,
-                                smem_desc(sV + st * TILE + kk * 2048, 16384, 1024), id_o, (acc || kk > 0) ? 1u : 0u);
+                for (int hk = 0; hk < 2; ++hk) {  // the first keys' products run while the others' weights are formed
+                    if (!mbar_wait(p_full + 16 * x + 8 * hk, par, abort_flag, a.status)) return false;
+                    tc_fence_after();
+                    mma4_ts(tmem + 256 + x * HD, tmem + 128 * x + 32 * hk, smem_desc(sV + st * TILE + hk * 8192, 16384, 1024), id_o,
+                            acc || hk > 0 ? 1u : 0u);
+                }
                 return true;
             };
-            for (; ok && w.x < w.x1; w.next(a, pre), ++k) {
+            for (; ok && w.x < w.x1; w.next(a), ++k) {
                 const bool two = w.toks > a.tt;
                 const int nblk = w.k1 - w.k0;
                 if (!mbar_wait(q_full, k & 1, abort_flag, a.status) || !ready(false, ki)) { ok = false; break; }
@@ -808,9 +913,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
             }
         }
-    } else {
+    } else if (warp < 8) {
         // ---------------- softmax: half x, TMEM lane quarter q, one row per thread
-        const int x = (warp - 2) >> 2, q = warp & 3;
+        const int x = warp >> 2, q = warp & 3;
         const int r = q * 32 + lane;
         const int rt = r / a.Hg;  // token of the half
         const bool in = r < a.tt * a.Hg;
@@ -818,40 +923,42 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t tS = tmem + lane_off + 128 * x, tO = tmem + lane_off + 256 + x * HD;
         uint32_t scnt = 0, ocnt = 0;
         int4 d = make_int4(0, 0, 0, 0);
-        for (; w.x < w.x1; w.next(a, pre)) {
+        for (; w.x < w.x1; w.next(a)) {
             if (w.unit >= x0 && w.unit + w.tiles > x1)
                 d = make_int4(w.row + w.tok0, w.g,
                               2 * (block_of(W, G, w.unit + w.tiles - 1) - (int)blockIdx.x + 1) + (w.unit == x0 ? 0 : 1), w.toks);
             if (x == 1 && w.toks <= a.tt) continue;
             const bool live = in && x * a.tt + rt < w.toks;
-            const int first = w.len - w.n + w.tok0 + x * a.tt;  // position of the half's first token
-            const int pos = live ? first + rt : -1;             // the last key that the row sees
+            const int k0 = w.k0, k1 = w.k1;
+            int first = w.len - w.n + w.tok0 + x * a.tt - k0 * 128;  // position of the half's first token, from the tile's first key
+            int lim = live ? first + rt : -1;                        // key c of the tile is visible iff c <= lim
+            // the unit's last tile, where it ends inside the tile, and its keys there
+            const int cut_tile = x == 0 && k1 == w.tiles && (w.end & 127) ? k1 - 1 : -1, cut_keys = w.end & 127;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
-            for (int kt = w.k0; kt < w.k1; ++kt) {
+            for (int kt = k0; kt < k1; ++kt, first -= 128, lim -= 128) {
                 if (!warp_wait(s_full + 8 * x, scnt & 1, abort_flag, a.status)) { ok = false; break; }
                 tc_fence_after();
-                const bool diag = kt * 128 + 127 > first;
-                const int lim = pos - kt * 128;  // key c of the tile is visible iff c <= lim
-                uint32_t sr[128];
-#pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4) tmem_ld32_issue(tS + 32 * q4, sr + 32 * q4);
-                if (x == 0 && kt == w.tiles - 1 && (w.end & 127)) {
-                    // the unit's last tile: values behind its keys are cleared (their weight is 0, but a page may
+                const bool diag = 127 > first;
+                if (kt == cut_tile) {
+                    // values behind the unit's keys are cleared (their weight is 0, but a page may
                     // hold anything there).  V_j is released after P(j) V_j, so its barrier is in this tile's phase.
-                    const int st = scnt % KVSTG, v0 = w.end & 127;
+                    const int st = scnt % KVSTG;
                     if (!warp_wait(v_full + 8 * st, (scnt / KVSTG) & 1, abort_flag, a.status)) ok = false;
                     if (ok) {
-                        for (int i = v0 * 8 + (warp - 2) * 32 + lane; i < 128 * 8; i += 128)
+                        for (int i = cut_keys * 8 + warp * 32 + lane; i < 128 * 8; i += 128)
 #pragma unroll
                             for (int c = 0; c < KB; ++c)
                                 *reinterpret_cast<uint4*>(smem_dyn + Lay::V + st * TILE + c * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
                         fence_proxy_async_smem();
                     }
                 }
+                if (!ok) break;
+                uint32_t sr[128];
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) tmem_ld32_issue(tS + 32 * q4, sr + 32 * q4);
                 ++scnt;
                 tmem_wait_ld();
-                if (!ok) break;
                 float mx4[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mx4[k] = -INFINITY;
@@ -867,102 +974,121 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 mx *= a.scale_log2;
-                const bool rescale = mx > m + 8.f;
+                const bool rescale = live && mx > m + 8.f;  // rows of nothing hold anything
                 const float mu = rescale ? mx : m;
                 const float alpha = rescale ? ex2(m - mx) : 1.f;
                 const float nmu = mu == -INFINITY ? 0.f : -mu;  // no key seen yet: every weight is 2^-inf = 0
                 const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), nmu2 = f2_pack(nmu, nmu);
+                if (kt > k0 && __any_sync(0xffffffffu, rescale)) {
+                    // O_x += P(j-1) V has completed (S(j) was issued after it and has landed);
+                    // O_x += P(j) V waits for this warp's hand-over below
+#pragma unroll 1
+                    for (int c = 0; c < HD; c += 8) {  // few at a time: the scores are live
+                        uint32_t o[8];
+                        tmem_ld8(tO + c, o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st8_nowait(tO + c, o);
+                    }
+                    tmem_wait_st();
+                }
                 uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                // P = 2^(s * scale - mu) as packed bf16 over the score columns, 64 keys handed over at a time
                 auto exp_pack = [&](auto poly) {
                     constexpr bool kPoly = decltype(poly)::value;
 #pragma unroll
-                    for (int q8 = 0; q8 < 8; ++q8) {
-                        uint32_t pk[8];
+                    for (int hk = 0; hk < 2; ++hk) {
 #pragma unroll
-                        for (int c = 0; c < 16; c += 2) {
-                            const int cc = 16 * q8 + c;
-                            float y0, y1;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, nmu2), y0, y1);
-                            if (!kPoly && diag) {
-                                if (cc > lim) y0 = -INFINITY;
-                                if (cc + 1 > lim) y1 = -INFINITY;
+                        for (int q8 = 4 * hk; q8 < 4 * hk + 4; ++q8) {
+                            uint32_t pk[8];
+#pragma unroll
+                            for (int c = 0; c < 16; c += 2) {
+                                const int cc = 16 * q8 + c;
+                                const uint64_t y = f2_fma(f2_pack(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, nmu2);
+                                float e0, e1;
+                                if (kPoly && (c / 2) * kPolyPairs % 8 < kPolyPairs) {
+                                    exp2_fma(y, e0, e1);
+                                } else {
+                                    float y0, y1;
+                                    f2_unpack(y, y0, y1);
+                                    if (!kPoly && diag) {
+                                        if (cc > lim) y0 = -INFINITY;
+                                        if (cc + 1 > lim) y1 = -INFINITY;
+                                    }
+                                    e0 = ex2(y0);
+                                    e1 = ex2(y1);
+                                }
+                                sum2[(c >> 1) & 1] = f2_add(sum2[(c >> 1) & 1], f2_pack(e0, e1));
+                                pk[c >> 1] = pack2(e0, e1);
                             }
-                            const float e0 = ex2(y0);
-                            const float e1 = (kPoly && (c / 2) % (kPolyEvery / 2) == kPolyEvery / 2 - 1) ? exp2_fma(y1) : ex2(y1);
-                            sum2[(c >> 1) & 1] = f2_add(sum2[(c >> 1) & 1], f2_pack(e0, e1));
-                            pk[c >> 1] = pack2(e0, e1);
+                            tmem_st8_nowait(tS + 8 * q8, pk);
                         }
-                        tmem_st8_nowait(tS + 8 * q8, pk);
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(p_full + 16 * x + 8 * hk);
                     }
                 };
                 if (!diag) exp_pack(std::true_type{});
                 else exp_pack(std::false_type{});
-                tmem_wait_st();
                 float s00, s01, s10, s11;
                 f2_unpack(sum2[0], s00, s01);
                 f2_unpack(sum2[1], s10, s11);
-                const float sum = (s00 + s01) + (s10 + s11);
-                if (kt > w.k0 && __any_sync(0xffffffffu, rescale)) {
-                    // O_x += P(j-1) V has completed (S(j) was issued after it and has landed);
-                    // O_x += P(j) V waits for this warp's hand-over below
-#pragma unroll 1
-                    for (int c = 0; c < HD / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32_issue(tO + c * 32, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st32(tO + c * 32, o);
-                        tmem_wait_st();
-                    }
-                }
-                l = l * alpha + sum;
+                l = l * alpha + ((s00 + s01) + (s10 + s11));
                 m = mu;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * x);
             }
             if (!ok || !warp_wait(o_full + 8 * x, ocnt & 1, abort_flag, a.status)) break;
             ++ocnt;
             tc_fence_after();
-            const bool whole = w.k0 == 0 && w.k1 == w.tiles;
-            if (whole) {
-                const float inv = 1.f / l;
-                bf16* orow = a.o + (size_t)(w.row + w.tok0 + (live ? x * a.tt + rt : 0)) * a.H * HD + (size_t)(w.g * a.Hg + r % a.Hg) * HD;
+            // Out by whole 128-byte lines: a warp's 32 rows x 128 bytes pass through shared memory (16-byte
+            // vectors exchanged by row, so that neither side meets in a bank), four rows to a store.
+            uint4* const pass = reinterpret_cast<uint4*>(smem_dyn + Lay::OUT + warp * 4096);
+            const bool whole = k0 == 0 && k1 == w.tiles;
+            const float inv = 1.f / l;
+            const size_t at = (size_t)(2 * blockIdx.x + (w.x == x0 ? 0 : 1)) * kChunkRows + x * 128 + r;
+            char* const mine = whole ? reinterpret_cast<char*>(a.o + (size_t)(w.row + w.tok0 + x * a.tt + rt) * a.H * HD + (size_t)(w.g * a.Hg + r % a.Hg) * HD)
+                                     : reinterpret_cast<char*>(a.part.o + at * HD);
+            const unsigned lives = __ballot_sync(0xffffffffu, live);
+            const int lines = HD * (whole ? 2 : 4) / 128;
 #pragma unroll 1
-                for (int c = 0; c < HD / 32; ++c) {
-                    float o[32];
-                    tmem_ld32(tO + c * 32, o);
-                    if (live) {
+            for (int c = 0; c < lines; ++c) {
+                if (whole) {
+#pragma unroll
+                    for (int hk = 0; hk < 2; ++hk) {
+                        float o[32];
+                        tmem_ld32(tO + 64 * c + 32 * hk, o);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<uint4*>(orow + c * 32 + 8 * i) =
+                            pass[lane * 8 + ((4 * hk + i) ^ (lane & 7))] =
                                 make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv), pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                                            pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
                     }
-                }
-            } else {
-                const size_t at = (size_t)(2 * blockIdx.x + (w.x == x0 ? 0 : 1)) * kChunkRows + x * 128 + r;
-                float* to = a.part.o + at * HD;
-#pragma unroll 1
-                for (int c = 0; c < HD / 32; ++c) {
-                    float o[32];
-                    tmem_ld32(tO + c * 32, o);
-                    if (live) {
+                } else {
+                    uint32_t o[32];
+                    tmem_ld32_issue(tO + 32 * c, o);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<float4*>(to + c * 32 + 4 * i) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        pass[lane * 8 + (i ^ (lane & 7))] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
-                if (live) a.part.ml[at] = make_float2(m, l);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 4 * i + (lane >> 3);
+                    char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), row));
+                    if (lives >> row & 1) *reinterpret_cast<uint4*>(to + 128 * c + 16 * (lane & 7)) = pass[row * 8 + ((lane & 7) ^ (row & 7))];
+                }
+                __syncwarp();
             }
+            if (!whole && live) a.part.ml[at] = make_float2(m, l);
+            tc_fence_before();
             // the next piece's first product overwrites O: it waits for this half's P, handed over after these reads
         }
-        if (threadIdx.x == 64) a.part.desc[blockIdx.x] = *abort_flag ? make_int4(0, 0, 0, 0) : d;
+        if (threadIdx.x == 0) a.part.desc[blockIdx.x] = *abort_flag ? make_int4(0, 0, 0, 0) : d;
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -1132,7 +1258,7 @@ cudaError_t attention(const bf16* qkv, int H, int nkv, int rows, int max_new, co
     if (chunks) {
         if ((e = ensure_smem_limit((const void*)paged_chunk_kernel<HD>, ChunkLayout<HD>::bytes(kMaxRequests))) != cudaSuccess) return e;
         const int tt = 128 / Hg;
-        jc = {partials(ws, G, kChunkRows, HD), kChunkRows, 128, tt, 8};
+        jc = {partials(ws, G, kChunkRows, HD), kChunkRows, 128, tt, 16};
         ChunkArgs a{kv, o, jc.part, H, nkv, Hg, tt, rows, std::min(kv.page, 128), max_new, decodes, scale_log2, status};
         CUtensorMap tq, tk, tv;
         const cuuint64_t ld = (cuuint64_t)(H + 2 * nkv) * HD * 2;
