@@ -24,7 +24,7 @@ using namespace tc;
 
 constexpr int kTile = 64;        // keys of a decode tile
 constexpr int kDecRows = 16;     // query heads of a K/V head that the decode kernel takes
-constexpr int kDecThreads = 288; // 8 consumer warps, then the producer
+constexpr int kDecThreads = 320; // 8 consumer warps, the producer, and one that writes the cache
 constexpr float kLog2eF = 1.44269504088896340736f;
 
 // Partial results of the G blocks, two pieces each.  `desc` tells of the unit that begins in a
@@ -144,9 +144,13 @@ struct DecLayout {
     // ahead, while the other's tile is still on its way, and see the phase before as its own.
     static constexpr int STAGES = HD == 128 ? 4 : 8;
     static_assert(STAGES % 2 == 0, "a stage belongs to one group of consumers");
-    static constexpr int RED = STAGES * STAGE;              // 4 warps' accumulators and statistics
-    static constexpr int RED_W = (HD / 2 + 4) * 32 * 4;
-    static constexpr int BAR = RED + 4 * RED_W;
+    static constexpr int QS = 3;                            // pieces whose query rows, and new k and v, are brought ahead
+    static constexpr int Q_BYTES = (kDecRows + 2) * HD * 2;
+    static constexpr int Q = STAGES * STAGE;
+    static constexpr int RED = Q + QS * Q_BYTES;            // 8 warps' outputs, 64 columns at a time
+    static constexpr int RED_LD = 68;                       // floats of a row
+    static constexpr int ML = RED + 8 * kDecRows * RED_LD * 4;  // [8][16] maximum, sum
+    static constexpr int BAR = ML + 8 * kDecRows * 8;
     static constexpr int PRE = BAR + 256;
     static constexpr int bytes(int n_req) { return PRE + (n_req + 1) * 4; }
 };
@@ -198,14 +202,19 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     pdl_trigger();
     const uint32_t base = smem_u32(smem_dyn);
     float* red = reinterpret_cast<float*>(smem_dyn + Lay::RED);
-    const uint32_t full = base + Lay::BAR, empty = full + 8 * ST;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_dyn + Lay::BAR + 16 * ST);
+    float2* red_ml = reinterpret_cast<float2*>(smem_dyn + Lay::ML);
+    const uint32_t full = base + Lay::BAR, empty = full + 8 * ST, q_full = empty + 8 * ST, q_empty = q_full + 8 * Lay::QS;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_dyn + Lay::BAR + 16 * (ST + Lay::QS));
     int* pre = reinterpret_cast<int*>(smem_dyn + Lay::PRE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int st = 0; st < ST; ++st) {
             mbar_init(full + 8 * st, 1);
             mbar_init(empty + 8 * st, 4);
+        }
+        for (int st = 0; st < Lay::QS; ++st) {
+            mbar_init(q_full + 8 * st, 1);
+            mbar_init(q_empty + 8 * st, 8);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -225,10 +234,21 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     if (warp == 8) {
         // ---------------- producer: a tile's pages, one copy per page piece
-        int i = 0;
+        int i = 0, k = 0;
         bool ok = true;
-        for (int x = x0; ok && x < x1;) {
+        for (int x = x0; ok && x < x1; ++k) {
             const DecSeg s = dec_seg(a, pre, x, x1);
+            ok = warp_wait(q_empty + 8 * (k % Lay::QS), ((k / Lay::QS) & 1) ^ 1, abort_flag, a.status);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t to = base + Lay::Q + (k % Lay::QS) * Lay::Q_BYTES, bar = q_full + 8 * (k % Lay::QS);
+                const bf16* from = a.qkv + (size_t)s.row * ((a.H + 2 * a.nkv) * HD);
+                mbar_expect_tx(bar, (uint32_t)(a.Hg + 2) * HD * 2);
+                bulk_load(to, from + (size_t)s.g * a.Hg * HD, (uint32_t)a.Hg * HD * 2, bar);
+                bulk_load(to + kDecRows * HD * 2, from + (size_t)(a.H + s.g) * HD, HD * 2, bar);
+                bulk_load(to + (kDecRows + 1) * HD * 2, from + (size_t)(a.H + a.nkv + s.g) * HD, HD * 2, bar);
+            }
+            __syncwarp();
             const int32_t* table = a.kv.table + (size_t)s.r * a.kv.max_blocks;
             const int per = kTile >> pshift;  // pieces of a tile
             int have = -1, entry = 0;         // 32 pieces' slots in the lanes, from piece `have` on
@@ -259,47 +279,75 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             x += s.k1 - s.k0;
         }
         if (!ok) {  // copies in flight land before the block exits
-            for (int k = max(0, i - ST); k < i; ++k) {
+            auto drain = [&](uint32_t bar, uint32_t parity) {
                 const uint64_t t0 = globaltimer();
-                while (!mbar_try(full + 8 * (k % ST), (k / ST) & 1) && globaltimer() - t0 < 1000000ull) {}
+                while (!mbar_try(bar, parity) && globaltimer() - t0 < 1000000ull) {}
+            };
+            for (int t = max(0, i - ST); t < i; ++t) drain(full + 8 * (t % ST), (t / ST) & 1);
+            for (int t = max(0, k + 1 - Lay::QS); t <= k; ++t) drain(q_full + 8 * (t % Lay::QS), (t / Lay::QS) & 1);
+        }
+        pdl_wait();
+        return;
+    }
+    if (warp == 9) {
+        // ---------------- every row's k, v to its slot, eight vectors of a thread on their way
+        constexpr int U = 8;
+        const int kvn = a.nkv * HD, per_row = kvn / 4;  // 16-byte vectors of k, then of v
+        const long long total = (long long)a.rows * per_row, step = (long long)gridDim.x * 32;
+        for (long long v0 = (long long)blockIdx.x * 32 + lane; v0 < total; v0 += U * step) {
+            int slot[U], e[U];
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const long long v = v0 + u * step;
+                slot[u] = -1;
+                if (v >= total) continue;
+                const int row = (int)(v / per_row);
+                e[u] = (int)(v % per_row) * 8;
+                slot[u] = a.slots[row];
+                x[u] = *reinterpret_cast<const uint4*>(a.qkv + (size_t)row * ((a.H + 2 * a.nkv) * HD) + (size_t)a.H * HD + e[u]);
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if ((unsigned)slot[u] < (unsigned)(a.kv.n_pages << shift))
+                    *reinterpret_cast<uint4*>(e[u] < kvn ? (bf16*)a.kv.k + (size_t)slot[u] * kvn + e[u]
+                                                         : (bf16*)a.kv.v + (size_t)slot[u] * kvn + (e[u] - kvn)) = x[u];
+                else if (slot[u] >= 0)
+                    set_status(a.status, ST_BAD_PAGE);
+            }
+        }
+        if (lane == 0) {
+            int4 d = make_int4(0, 0, 0, 0);
+            if (x0 < x1) {
+                const DecSeg s = dec_seg(a, pre, x1 - 1, x1);  // the block's last (request, K/V head)
+                const long long end = s.unit + s.tiles;
+                if (s.unit >= x0 && end > x1)
+                    d = make_int4(s.row, s.g, 2 * (block_of(W, G, end - 1) - (int)blockIdx.x + 1) + (s.unit == x0 ? 0 : 1), 1);
+            }
+            a.part.desc[blockIdx.x] = d;
         }
         pdl_wait();
         return;
     }
 
     // ---------------- consumers
-    {   // every row's k, v to its slot, while the first tiles are on their way
-        const int kvn = a.nkv * HD, per_row = kvn / 4;  // 16-byte vectors of k, then of v
-        const long long total = (long long)a.rows * per_row;
-        for (long long v = (long long)blockIdx.x * 256 + threadIdx.x; v < total; v += (long long)gridDim.x * 256) {
-            const int row = (int)(v / per_row), e = (int)(v % per_row) * 8;
-            const int slot = a.slots[row];
-            if ((unsigned)slot >= (unsigned)(a.kv.n_pages << shift)) {
-                if (slot >= 0) set_status(a.status, ST_BAD_PAGE);
-                continue;
-            }
-            const bf16* src = a.qkv + (size_t)row * ((a.H + 2 * a.nkv) * HD) + (size_t)a.H * HD + e;
-            bf16* dst = e < kvn ? (bf16*)a.kv.k + (size_t)slot * kvn + e : (bf16*)a.kv.v + (size_t)slot * kvn + (e - kvn);
-            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-        }
-    }
     const int grp = warp >> 2, w = warp & 3;
-    int i = 0;
+    int i = 0, piece = 0;
     bool ok = true;
-    for (int x = x0; x < x1;) {
+    for (int x = x0; x < x1; ++piece) {
         const DecSeg s = dec_seg(a, pre, x, x1);
-        const size_t qrow = (size_t)s.row * ((a.H + 2 * a.nkv) * HD);
+        const uint32_t q_at = Lay::Q + (piece % Lay::QS) * Lay::Q_BYTES;  // query rows, then the new k and v
+        if (ok) ok = warp_wait(q_full + 8 * (piece % Lay::QS), (piece / Lay::QS) & 1, abort_flag, a.status);
         uint32_t q[HD / 16][4];
         {
-            const bf16* p0 = a.qkv + qrow + (size_t)(s.g * a.Hg + (lane >> 2)) * HD + (lane & 3) * 2;
+            const uint8_t* p0 = smem_dyn + q_at + (lane >> 2) * (HD * 2) + (lane & 3) * 4;
             const bool lo = (lane >> 2) < a.Hg, hi = (lane >> 2) + 8 < a.Hg;
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k) {
-                q[k][0] = lo ? *reinterpret_cast<const uint32_t*>(p0 + 16 * k) : 0u;
-                q[k][1] = hi ? *reinterpret_cast<const uint32_t*>(p0 + 8 * HD + 16 * k) : 0u;
-                q[k][2] = lo ? *reinterpret_cast<const uint32_t*>(p0 + 16 * k + 8) : 0u;
-                q[k][3] = hi ? *reinterpret_cast<const uint32_t*>(p0 + 8 * HD + 16 * k + 8) : 0u;
+                q[k][0] = lo ? *reinterpret_cast<const uint32_t*>(p0 + 32 * k) : 0u;
+                q[k][1] = hi ? *reinterpret_cast<const uint32_t*>(p0 + 16 * HD + 32 * k) : 0u;
+                q[k][2] = lo ? *reinterpret_cast<const uint32_t*>(p0 + 32 * k + 16) : 0u;
+                q[k][3] = hi ? *reinterpret_cast<const uint32_t*>(p0 + 16 * HD + 32 * k + 16) : 0u;
             }
         }
         float acc[NB][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -321,12 +369,11 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     for (int v = lane; v < (16 - valid) * (HD / 8); v += 32)
                         *reinterpret_cast<uint4*>(smem_dyn + (sv - base) + dec_at<HD>(w * 16 + valid + v / (HD / 8), v % (HD / 8), pshift)) =
                             make_uint4(0, 0, 0, 0);
-                    const bf16* src = a.qkv + qrow + (size_t)(a.H + s.g) * HD;
                     for (int v = lane; v < 2 * (HD / 8); v += 32) {
                         const bool isv = v >= HD / 8;
                         const int j = isv ? v - HD / 8 : v;
                         *reinterpret_cast<uint4*>(smem_dyn + ((isv ? sv : sk) - base) + dec_at<HD>(w * 16 + valid - 1, j, pshift)) =
-                            *reinterpret_cast<const uint4*>(src + (isv ? (size_t)a.nkv * HD : 0) + 8 * j);
+                            *reinterpret_cast<const uint4*>(smem_dyn + q_at + kDecRows * HD * 2 + 16 * v);
                     }
                     __syncwarp();
                 }
@@ -398,72 +445,56 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
         }
-        // the warps' outputs into one, the upper half of them at a time (the same order always)
-#pragma unroll
-        for (int half = 4; half > 0; half >>= 1) {
-            if (warp >= half && warp < 2 * half) {
-                float* to = red + (warp - half) * (Lay::RED_W / 4) + lane;
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) to[(4 * n + e) * 32] = acc[n][e];
-                to[(4 * NB) * 32] = m[0]; to[(4 * NB + 1) * 32] = m[1];
-                to[(4 * NB + 2) * 32] = l[0]; to[(4 * NB + 3) * 32] = l[1];
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (warp < half) {
-                const float* from = red + warp * (Lay::RED_W / 4) + lane;
-                float c0[2], c1[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float om = from[(4 * NB + h) * 32], ol = from[(4 * NB + 2 + h) * 32];
-                    const float M = fmaxf(m[h], om);
-                    c0[h] = m[h] == -INFINITY ? 0.f : ex2(m[h] - M);
-                    c1[h] = om == -INFINITY ? 0.f : ex2(om - M);
-                    l[h] = l[h] * c0[h] + ol * c1[h];
-                    m[h] = M;
-                }
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[n][e] = acc[n][e] * c0[e >> 1] + from[(4 * n + e) * 32] * c1[e >> 1];
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_empty + 8 * (piece % Lay::QS));
+        // the warps' outputs into one, 64 columns at a time, the warps always in the same order
+        if ((lane & 3) == 0) {
+            red_ml[warp * kDecRows + (lane >> 2)] = make_float2(m[0], l[0]);
+            red_ml[warp * kDecRows + 8 + (lane >> 2)] = make_float2(m[1], l[1]);
         }
-        if (warp == 0 && ok) {
-            const bool whole = s.k0 == 0 && s.k1 == s.tiles;
-            const int slot = 2 * (int)blockIdx.x + (x == x0 ? 0 : 1);
+        const bool whole = s.k0 == 0 && s.k1 == s.tiles;
+        const int slot = 2 * (int)blockIdx.x + (x == x0 ? 0 : 1);
+        const int row = threadIdx.x >> 4, col = (threadIdx.x & 15) * 4;  // of the joined output, and 64 c more columns
+        float f[8], L = 0.f, M = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int hr = (lane >> 2) + 8 * h;
-                if (hr >= a.Hg) continue;
-                if (whole) {
-                    const float inv = 1.f / l[h];
-                    bf16* to = a.o + (size_t)s.row * a.H * HD + (size_t)(s.g * a.Hg + hr) * HD + (lane & 3) * 2;
+        for (int c = 0; c < HD / 64; ++c) {
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-                        *reinterpret_cast<uint32_t*>(to + 8 * n) = pack2(acc[n][2 * h] * inv, acc[n][2 * h + 1] * inv);
-                } else {
-                    float* to = a.part.o + ((size_t)slot * kDecRows + hr) * HD + (lane & 3) * 2;
+            for (int n = 0; n < 8; ++n) {
+                float* to = red + (warp * kDecRows + (lane >> 2)) * Lay::RED_LD + 8 * n + 2 * (lane & 3);
+                *reinterpret_cast<float2*>(to) = make_float2(acc[8 * c + n][0], acc[8 * c + n][1]);
+                *reinterpret_cast<float2*>(to + 8 * Lay::RED_LD) = make_float2(acc[8 * c + n][2], acc[8 * c + n][3]);
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (c == 0) {
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-                        *reinterpret_cast<float2*>(to + 8 * n) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
-                    if ((lane & 3) == 0) a.part.ml[(size_t)slot * kDecRows + hr] = make_float2(m[h], l[h]);
+                for (int k = 0; k < 8; ++k) M = fmaxf(M, red_ml[k * kDecRows + row].x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 ml = red_ml[k * kDecRows + row];
+                    f[k] = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+                    L += ml.y * f[k];
                 }
             }
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(red + (k * kDecRows + row) * Lay::RED_LD + col);
+                o.x = fmaf(v.x, f[k], o.x); o.y = fmaf(v.y, f[k], o.y);
+                o.z = fmaf(v.z, f[k], o.z); o.w = fmaf(v.w, f[k], o.w);
+            }
+            if (row < a.Hg && ok) {
+                if (whole) {
+                    const float inv = 1.f / L;
+                    *reinterpret_cast<uint2*>(a.o + (size_t)s.row * a.H * HD + (size_t)(s.g * a.Hg + row) * HD + 64 * c + col) =
+                        make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+                } else {
+                    *reinterpret_cast<float4*>(a.part.o + ((size_t)slot * kDecRows + row) * HD + 64 * c + col) = o;
+                    if (c == 0 && col == 0) a.part.ml[(size_t)slot * kDecRows + row] = make_float2(M, L);
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
         }
         x += s.k1 - s.k0;
-    }
-    if (threadIdx.x == 0) {
-        int4 d = make_int4(0, 0, 0, 0);
-        if (x0 < x1 && ok) {
-            const DecSeg s = dec_seg(a, pre, x1 - 1, x1);  // the block's last (request, K/V head)
-            const long long end = s.unit + s.tiles;
-            if (s.unit >= x0 && end > x1)
-                d = make_int4(s.row, s.g, 2 * (block_of(W, G, end - 1) - (int)blockIdx.x + 1) + (s.unit == x0 ? 0 : 1), 1);
-        }
-        a.part.desc[blockIdx.x] = d;
     }
     pdl_wait();
 }
@@ -487,6 +518,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 // attention is.
 constexpr int kChunkThreads = 320;  // softmax of half a, of half b (a warpgroup each); producer, MMA, two idle warps
 constexpr int kChunkRows = 256;
+constexpr int kWholeTiles = 10;  // units of so many key tiles are not cut: 8 requests of some 900 positions 33.9 -> 30.5 us
 constexpr int kPolyPairs = 1;  // pairs of scores, of every eight, that take 2^x from the FMA pipe
 
 struct ChunkArgs {
@@ -559,6 +591,7 @@ __device__ __forceinline__ long long ChunkArgs::tiles(int r) const {
 struct ChunkWalk {
     long long x, x1, unit;     // unit: the current unit's first tile in the line
     int r, g, b, row, n, len;  // request, K/V head, unit of the chunk; its first packed row, new rows, length
+    bool whole;                // pieces are whole units: those that begin in the part
     int tok0, toks, end, tiles, k0, k1;  // the unit's tokens [tok0, tok0 + toks), keys and tiles; the piece's tiles
 
     __device__ __forceinline__ void set(const ChunkArgs& a) {
@@ -569,8 +602,9 @@ struct ChunkWalk {
     }
     // Out of line, so that the walk's state waits in local memory while a piece is worked on.
     // By whole warps: the lanes look at a group's requests, then at 32 units, at once.
-    __device__ __forceinline__ void start(const ChunkArgs& a, const long long* pre, long long from, long long to) {
+    __device__ __forceinline__ void start(const ChunkArgs& a, const long long* pre, long long from, long long to, bool units) {
         x = from; x1 = to;
+        whole = units;
         if (x >= x1) return;
         const int lane = threadIdx.x & 31, groups = (a.kv.n_req + kGroup - 1) / kGroup;
         const int gr = find_request(pre, groups, x);
@@ -604,7 +638,8 @@ struct ChunkWalk {
         set(a);
         k0 = (int)rem;
         unit = x - k0;
-        k1 = (int)min((long long)tiles, k0 + (x1 - x));
+        k1 = whole ? tiles : (int)min((long long)tiles, k0 + (x1 - x));
+        if (whole && k0 > 0) next(a);  // it began in the block before
     }
     __device__ __forceinline__ void next(const ChunkArgs& a) {
         x += k1 - k0;
@@ -621,7 +656,7 @@ struct ChunkWalk {
         set(a);
         unit = x;
         k0 = 0;
-        k1 = (int)min((long long)tiles, x1 - x);
+        k1 = whole ? tiles : (int)min((long long)tiles, x1 - x);
     }
 };
 
@@ -733,9 +768,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tma_prefetch(&tm_v);
     }
     const int groups = (a.kv.n_req + kGroup - 1) / kGroup;
+    bool cuts = false;
     for (int base = 0; base < groups * kGroup; base += kChunkThreads) {
         const int r = base + (int)threadIdx.x;
         long long t = a.tiles(r);
+        cuts |= t > 0 && a.kv.kv_len[r] > 128 * kWholeTiles;
         if (blockIdx.x == 0 && r < a.kv.n_req) {
             int lo, n, len;
             if (!request(a.kv, a.rows, r, lo, n, len) || (a.max_new > 0 && n > a.max_new)) set_status(a.status, ST_BAD_LENGTH);
@@ -744,7 +781,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int o = kGroup / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
         if (r % kGroup == 0 && r / kGroup < groups) pre[r / kGroup] = t;
     }
-    __syncthreads();
+    // Short units are not cut: a piece saved would cost more to join than it takes.
+    const bool units = !__syncthreads_or(cuts);
     if (warp == 0) {  // exclusive prefix sums, 32 groups at a time
         long long run = 0;
         for (int base = 0; base < groups; base += 32) {
@@ -778,7 +816,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // outputs O in [256, 256 + HD) and [256 + HD, 256 + 2 HD)
 
     ChunkWalk w;
-    w.start(a, pre, x0, x1);
+    w.start(a, pre, x0, x1, units);
     if (warp == 8) {
         const int pshift = 31 - __clz(a.piece), shift = 31 - __clz(a.kv.page);
         const int per = 128 >> pshift;  // pieces of a tile
@@ -924,7 +962,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         uint32_t scnt = 0, ocnt = 0;
         int4 d = make_int4(0, 0, 0, 0);
         for (; w.x < w.x1; w.next(a)) {
-            if (w.unit >= x0 && w.unit + w.tiles > x1)
+            if (!w.whole && w.unit >= x0 && w.unit + w.tiles > x1)
                 d = make_int4(w.row + w.tok0, w.g,
                               2 * (block_of(W, G, w.unit + w.tiles - 1) - (int)blockIdx.x + 1) + (w.unit == x0 ? 0 : 1), w.toks);
             if (x == 1 && w.toks <= a.tt) continue;
@@ -1258,7 +1296,7 @@ cudaError_t attention(const bf16* qkv, int H, int nkv, int rows, int max_new, co
     if (chunks) {
         if ((e = ensure_smem_limit((const void*)paged_chunk_kernel<HD>, ChunkLayout<HD>::bytes(kMaxRequests))) != cudaSuccess) return e;
         const int tt = 128 / Hg;
-        jc = {partials(ws, G, kChunkRows, HD), kChunkRows, 128, tt, 16};
+        jc = {partials(ws, G, kChunkRows, HD), kChunkRows, 128, tt, 32};
         ChunkArgs a{kv, o, jc.part, H, nkv, Hg, tt, rows, std::min(kv.page, 128), max_new, decodes, scale_log2, status};
         CUtensorMap tq, tk, tv;
         const cuuint64_t ld = (cuuint64_t)(H + 2 * nkv) * HD * 2;
