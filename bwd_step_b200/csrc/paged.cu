@@ -92,11 +92,12 @@ __device__ __forceinline__ int row_request(const int* cu, int n_req, int i) {
     return lo;
 }
 
-__device__ __forceinline__ void plan_row(const PlanArgs& p, const int* cu, int shift, int i) {
+// (kept: the requests' kept positions, or null: read what the plan wrote)
+__device__ __forceinline__ void plan_row(const PlanArgs& p, const int* cu, const int* kept, int shift, int i) {
     int pos = 0, slot = -1;
     if (i < cu[p.n_req]) {
         const int r = row_request(cu, p.n_req, i);
-        pos = p.kv_len[r] - (cu[r + 1] - i);
+        pos = kept ? kept[r] + (i - cu[r]) : p.kv_len[r] - (cu[r + 1] - i);
         const int page = p.table[(size_t)r * p.max_blocks + (pos >> shift)];
         if ((unsigned)page < (unsigned)p.n_pages) slot = (page << shift) + (pos & (p.page - 1));
         else set_status(p.status, ST_BAD_PAGE);  // the stack of free pages held something else
@@ -105,64 +106,100 @@ __device__ __forceinline__ void plan_row(const PlanArgs& p, const int* cu, int s
     p.slots[i] = slot;
 }
 
-// One block.  Lengths to shared memory; per request the blocks that need a page
-// and the pages that it gives back; their prefix sums; then pages go back onto
-// the stack and are taken from its top, each at the place that its prefix names,
-// so that the result does not depend on timing.  Bound by latency: the chain
-// lengths -> table -> stack -> table -> rows of dependent global accesses.
+// One block.  Per request, the blocks that need a page and the pages that it gives
+// back; their prefix sums; then pages go back onto the stack and are taken from its
+// top, each at the place that its prefix names, so that the result does not depend on
+// timing.  Bound by latency, the chain lengths -> table -> stack -> table -> rows of
+// dependent global accesses, so every stage has all of its loads on their way at
+// once: a thread's requests with up to kPlanOwn blocks each, and for the others (long
+// chunks, released requests) a warp with kPlanWide blocks.
+constexpr int kPlanPer = kMaxRequests / kPlanThreads;  // requests of a thread
+constexpr int kPlanWide = 8 * 32;
+static_assert(kPlanOwn * kPlanPer <= 32, "a thread's blocks without a page are bits of a word");
+
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs p, bool fill_rows) {
     extern __shared__ int sm[];
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_specials;
     __shared__ unsigned long long s_rows;
     int* s_cached = sm;                  // positions kept of every request (0 when released)
     int* s_new = s_cached + p.n_req;     // its new positions
     int* s_need = s_new + p.n_req;       // its blocks without a page, then their prefix
     int* s_back = s_need + p.n_req;      // pages it gives back, then their prefix
     int* s_cu = s_back + p.n_req;        // [n_req + 1]
+    int* s_special = s_cu + p.n_req + 1; // requests that a warp looks after, 2 r + (released)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = kPlanThreads / 32;
     const int shift = 31 - __clz(p.page);
     const long long cap = (long long)p.max_blocks << shift;
     auto held = [&](int e) { return (unsigned)e < (unsigned)p.n_pages; };
-    auto released = [&](int r) { return p.release && p.release[r] != 0; };
-    if (tid == 0) { s_bad = 0; s_rows = 0; }
+    auto row_of = [&](int r) { return p.table + (size_t)r * p.max_blocks; };
+    auto first = [&](int r) { return s_cached[r] >> shift; };
+    auto end = [&](int r) { return (int)(((long long)s_cached[r] + s_new[r] + p.page - 1) >> shift); };
+    // a warp's blocks lo .. hi - 1 of a row, kPlanWide at a time: f(entries, first block)
+    auto blocks = [&](const int32_t* row, int lo, int hi, auto f) {
+        for (int j0 = lo; j0 < hi; j0 += kPlanWide) {
+            int e[kPlanWide / 32];
+#pragma unroll
+            for (int u = 0; u < kPlanWide / 32; ++u) e[u] = j0 + 32 * u + lane < hi ? row[j0 + 32 * u + lane] : -1;
+            f(e, j0);
+        }
+    };
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) { s_bad = 0; s_rows = 0; s_specials = 0; }
     const int count0 = *p.free_count;
     const int count = min(max(count0, 0), p.n_pages);
-    __syncthreads();
-    for (int r = tid; r < p.n_req; r += kPlanThreads) {
-        const int cached = p.cached[r], nw = p.new_len[r];
-        const bool rel = released(r);
-        const long long total = (long long)(rel ? 0 : cached) + nw;
-        const bool bad = cached < 0 || nw < 0 || total > cap || nw > p.rows;
-        if (bad) s_bad = ST_BAD_LENGTH;
-        s_cached[r] = bad || rel ? 0 : cached;
-        s_new[r] = s_cu[r] = bad ? 0 : nw;
-        if (!bad && nw) atomicAdd(&s_rows, (unsigned long long)nw);
-        // a short run of blocks is checked here, all loads in flight together
-        const int lo = s_cached[r] >> shift, hi = bad ? lo : (int)((total + p.page - 1) >> shift);
-        int need = 0;
-        if (rel || hi - lo > kPlanOwn) need = -1;
-        else
+    int cached[kPlanPer], fresh[kPlanPer], gone[kPlanPer];
 #pragma unroll
-            for (int j = 0; j < kPlanOwn; ++j)
-                need += lo + j < hi && !held(p.table[(size_t)r * p.max_blocks + lo + j]);
-        s_need[r] = need;
-        s_back[r] = 0;
+    for (int i = 0; i < kPlanPer; ++i) {
+        const int r = tid + i * kPlanThreads;
+        if (r >= p.n_req) break;
+        cached[i] = p.cached[r];
+        fresh[i] = p.new_len[r];
+        gone[i] = p.release ? p.release[r] : 0;
     }
     __syncthreads();
-    for (int r = warp; r < p.n_req; r += nwarp) {
-        if (s_need[r] >= 0) continue;
-        const int32_t* row = p.table + (size_t)r * p.max_blocks;
-        const int lo = s_cached[r] >> shift, hi = (int)(((long long)s_cached[r] + s_new[r] + p.page - 1) >> shift);
-        int n = 0;
-        if (released(r)) {
-            for (int j = lane; j < p.max_blocks; j += 32) n += held(row[j]);
+    unsigned want = 0;  // bit kPlanOwn i + j: block j of the thread's i-th request needs a page
+    unsigned long long rows = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i) {
+        const int r = tid + i * kPlanThreads;
+        if (r >= p.n_req) break;
+        const bool rel = gone[i] != 0;
+        const long long total = (long long)(rel ? 0 : cached[i]) + fresh[i];
+        const bool bad = cached[i] < 0 || fresh[i] < 0 || total > cap || fresh[i] > p.rows;
+        if (bad) s_bad = ST_BAD_LENGTH;
+        const int kept = bad || rel ? 0 : cached[i], n = bad ? 0 : fresh[i];
+        s_cached[r] = kept;
+        s_new[r] = s_cu[r] = n;
+        rows += n;
+        const int lo = kept >> shift, hi = bad ? lo : (int)((total + p.page - 1) >> shift);
+        s_need[r] = s_back[r] = 0;
+        if (!bad && (rel || hi - lo > kPlanOwn)) {
+            s_special[atomicAdd(&s_specials, 1)] = 2 * r + rel;
         } else {
-            for (int j = lo + lane; j < hi; j += 32) n += !held(row[j]);
+            int need = 0;
+#pragma unroll
+            for (int j = 0; j < kPlanOwn; ++j)
+                if (lo + j < hi && !held(row_of(r)[lo + j])) need |= 1 << j;
+            want |= (unsigned)need << (kPlanOwn * i);
+            s_need[r] = __popc(need);
         }
+    }
+    for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    if (lane == 0 && rows) atomicAdd(&s_rows, rows);
+    __syncthreads();
+    const int specials = s_specials;  // in any order: what comes of them goes by the prefix sums
+    for (int i = warp; i < specials; i += nwarp) {
+        const int r = s_special[i] >> 1;
+        const bool rel = s_special[i] & 1;
+        int n = 0;
+        blocks(row_of(r), rel ? 0 : first(r), rel ? p.max_blocks : end(r), [&](const int* e, int j0) {
+#pragma unroll
+            for (int u = 0; u < kPlanWide / 32; ++u) n += rel ? held(e[u]) : j0 + 32 * u + lane < end(r) && !held(e[u]);
+        });
         n = __reduce_add_sync(0xffffffffu, n);
         if (lane == 0) {
-            if (released(r)) { s_back[r] = n; s_need[r] = hi; }
-            else s_need[r] = n;
+            s_need[r] = rel ? end(r) : n;
+            s_back[r] = rel ? n : 0;
         }
     }
     __syncthreads();
@@ -185,47 +222,64 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     }
     if (tid == 0) {
         s_cu[p.n_req] = (int)s_rows;
+        *p.free_count = grown - need_all;
         if (count != count0 || count + back_all > p.n_pages) set_status(p.status, ST_BAD_PAGE);
     }
-    if (back_all) {
-        for (int r = warp; r < p.n_req; r += nwarp) {
-            if (!released(r)) continue;
-            int32_t* row = p.table + (size_t)r * p.max_blocks;
+    if (back_all)
+        for (int i = warp; i < specials; i += nwarp) {
+            if (!(s_special[i] & 1)) continue;
+            const int r = s_special[i] >> 1;
             int at = count + s_back[r];
-            for (int j0 = 0; j0 < p.max_blocks; j0 += 32) {
-                const int e = j0 + lane < p.max_blocks ? row[j0 + lane] : -1;
-                const unsigned m = __ballot_sync(0xffffffffu, held(e));
-                if (held(e)) {
-                    const int to = at + __popc(m & ((1u << lane) - 1));
-                    if (to < p.n_pages) p.free_pages[to] = e;
-                    row[j0 + lane] = -1;
+            blocks(row_of(r), 0, p.max_blocks, [&](const int* e, int j0) {
+#pragma unroll
+                for (int u = 0; u < kPlanWide / 32; ++u) {
+                    const unsigned m = __ballot_sync(0xffffffffu, held(e[u]));
+                    if (held(e[u])) {
+                        const int to = at + __popc(m & ((1u << lane) - 1));
+                        if (to < p.n_pages) p.free_pages[to] = e[u];
+                        row_of(r)[j0 + 32 * u + lane] = -1;
+                    }
+                    at += __popc(m);
                 }
-                at += __popc(m);
-            }
+            });
         }
-    }
     __syncthreads();
     if (need_all) {
-        for (int r = tid; r < p.n_req; r += kPlanThreads) {
-            const int lo = s_cached[r] >> shift, hi = (s_cached[r] + s_new[r] + p.page - 1) >> shift;
-            if (hi - lo > kPlanOwn) continue;
-            int32_t* row = p.table + (size_t)r * p.max_blocks;
+        int page[kPlanPer * kPlanOwn];
+#pragma unroll
+        for (int i = 0; i < kPlanPer; ++i) {
+            const int r = tid + i * kPlanThreads;
+            if (r >= p.n_req) break;
             int from = grown - 1 - s_need[r];
 #pragma unroll
             for (int j = 0; j < kPlanOwn; ++j)
-                if (lo + j < hi && !held(row[lo + j])) row[lo + j] = p.free_pages[from--];
+                if (want >> (kPlanOwn * i + j) & 1) page[kPlanOwn * i + j] = p.free_pages[from--];
         }
-        for (int r = warp; r < p.n_req; r += nwarp) {
-            const int lo = s_cached[r] >> shift, hi = (s_cached[r] + s_new[r] + p.page - 1) >> shift;
-            if (hi - lo <= kPlanOwn) continue;
-            int32_t* row = p.table + (size_t)r * p.max_blocks;
+#pragma unroll
+        for (int i = 0; i < kPlanPer; ++i) {
+            const int r = tid + i * kPlanThreads;
+            if (r >= p.n_req) break;
+#pragma unroll
+            for (int j = 0; j < kPlanOwn; ++j)
+                if (want >> (kPlanOwn * i + j) & 1) row_of(r)[first(r) + j] = page[kPlanOwn * i + j];
+        }
+        for (int i = warp; i < specials; i += nwarp) {
+            const int r = s_special[i] >> 1;
+            const bool rel = s_special[i] & 1;  // its row is empty by now
             int from = grown - 1 - s_need[r];
-            for (int j0 = lo; j0 < hi; j0 += 32) {
-                const bool want = j0 + lane < hi && !held(row[j0 + lane]);
-                const unsigned m = __ballot_sync(0xffffffffu, want);
-                if (want) row[j0 + lane] = p.free_pages[from - __popc(m & ((1u << lane) - 1))];
-                from -= __popc(m);
-            }
+            blocks(row_of(r), first(r), end(r), [&](const int* e, int j0) {
+                int got[kPlanWide / 32];
+#pragma unroll
+                for (int u = 0; u < kPlanWide / 32; ++u) {
+                    const bool need = j0 + 32 * u + lane < end(r) && (rel || !held(e[u]));
+                    const unsigned m = __ballot_sync(0xffffffffu, need);
+                    got[u] = need ? p.free_pages[from - __popc(m & ((1u << lane) - 1))] : -1;
+                    from -= __popc(m);
+                }
+#pragma unroll
+                for (int u = 0; u < kPlanWide / 32; ++u)
+                    if (j0 + 32 * u + lane < end(r) && (rel || !held(e[u]))) row_of(r)[j0 + 32 * u + lane] = got[u];
+            });
         }
     }
     for (int r = tid; r <= p.n_req; r += kPlanThreads) {
@@ -233,19 +287,19 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
         if (r < p.n_req) p.kv_len[r] = s_cached[r] + s_new[r];
     }
     __syncthreads();
-    if (tid == 0) *p.free_count = grown - need_all;
     if (fill_rows)
-        for (int i = tid; i < p.rows; i += kPlanThreads) plan_row(p, s_cu, shift, i);
+        for (int i = tid; i < p.rows; i += kPlanThreads) plan_row(p, s_cu, s_cached, shift, i);
 }
 
 // Positions and slots of the rows, over many blocks.
 __global__ void __launch_bounds__(256) page_rows_kernel(const PlanArgs p) {
     extern __shared__ int s_cu[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
     for (int r = threadIdx.x; r <= p.n_req; r += blockDim.x) s_cu[r] = p.cu_rows[r];
     __syncthreads();
     const int shift = 31 - __clz(p.page);
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.rows; i += gridDim.x * blockDim.x)
-        plan_row(p, s_cu, shift, i);
+        plan_row(p, s_cu, nullptr, shift, i);
 }
 
 // ---------------------------------------------------------------- cache writes
@@ -478,14 +532,24 @@ cudaError_t launch_page_plan(int n_req, int page, int max_blocks, int n_pages, i
                              int32_t* slots, int* status, cudaStream_t s) {
     const PlanArgs p{n_req, page, max_blocks, n_pages, rows, cached, new_len, release, table, free_pages, free_count,
                      cu_rows, kv_len, positions, slots, status};
-    cudaError_t e = ensure_smem_limit((const void*)page_plan_kernel, (5 * kMaxRequests + 1) * 4);
+    cudaError_t e = ensure_smem_limit((const void*)page_plan_kernel, (6 * kMaxRequests + 1) * 4);
     if (e != cudaSuccess) return e;
     const bool fused = rows <= kPlanFusedRows;
-    page_plan_kernel<<<1, kPlanThreads, (5 * n_req + 1) * 4, s>>>(p, fused);
+    page_plan_kernel<<<1, kPlanThreads, (6 * n_req + 1) * 4, s>>>(p, fused);
     count_launch();
     if (!fused) {
         const int blocks = std::min((rows + 255) / 256, 4 * device_sm_count());
-        page_rows_kernel<<<blocks, 256, (n_req + 1) * 4, s>>>(p);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(blocks);
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = (n_req + 1) * 4;
+        cfg.stream = s;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        if ((e = cudaLaunchKernelEx(&cfg, page_rows_kernel, p)) != cudaSuccess) return e;
         count_launch();
     }
     return cudaGetLastError();
