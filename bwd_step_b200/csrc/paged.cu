@@ -334,49 +334,83 @@ __global__ void __launch_bounds__(128) last_rows_kernel(const A* __restrict__ x,
 }
 
 // ---------------------------------------------------------------- plain attention
-// One block per (packed row, query head), four warps over the keys, 32 keys of a
-// warp at a time: each lane forms one key's whole score, the warp keeps a running
-// maximum and sum, and the lanes then own HD/32 output dims each while the 32
-// weights and slots pass by shuffles.  The four warps are joined at the end.
+// Request of packed row i < cu[n_req], by a whole warp, 32 ways at a time.
+__device__ __forceinline__ int row_request_warp(const int32_t* __restrict__ cu, int n_req, int i, int lane) {
+    int lo = 0, hi = n_req;  // cu[lo] <= i < cu[hi]
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned m = __ballot_sync(0xffffffffu, at < hi && cu[at] <= i);
+        const int k = m ? 31 - __clz(m) : 0;
+        hi = min(hi, lo + (k + 1) * step);
+        lo += k * step;
+    }
+    return lo;
+}
+
+// Heads and types that the tensor-core kernels do not take.  One block per (packed row,
+// query head), four warps over the keys, 32 keys of a warp at a time: each lane forms
+// one key's whole score, the warp keeps a running maximum and sum, and the lanes then
+// own output dims while the 32 weights pass by shuffles.  The four warps are joined at
+// the end.  The step's own keys and values are read from its rows, not from the cache,
+// so the same launch writes them there.  Bound by latency at the sizes of such models
+// (five requests of some 100 positions, 4 heads of 16: see the launch's time).
 template <typename A, int HD>
-__global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restrict__ qkv, int H, int nkv,
-                                                              const A* __restrict__ kc, const A* __restrict__ vc,
-                                                              const PagedKv kv, float scale_log2, A* __restrict__ o,
-                                                              int* status) {
+__global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restrict__ qkv, int H, int nkv, int rows,
+                                                              const int32_t* __restrict__ slots, const PagedKv kv,
+                                                              float scale_log2, A* __restrict__ o, int* status) {
     constexpr int VEC = Vec<A>::N;
     constexpr int EPL = HD >= 32 ? HD / 32 : 1;
+    constexpr int WAYS = HD >= 32 ? 1 : 32 / HD;  // keys that a warp's lanes take at once in the second product
     __shared__ float sq[HD], sm[4], sl[4], so[4][HD];
-    __shared__ int s_r;
     const int row = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) s_r = row < kv.cu_rows[kv.n_req] && row >= kv.cu_rows[0] ? row_request(kv.cu_rows, kv.n_req, row) : -1;
-    const int Nqkv = (H + 2 * nkv) * HD;
+    const int Nqkv = (H + 2 * nkv) * HD, kvn = nkv * HD;
+    A* const kc = reinterpret_cast<A*>(kv.k);
+    A* const vc = reinterpret_cast<A*>(kv.v);
+    if (h == 0) {
+        const int slot = slots[row];
+        if ((unsigned)slot < (unsigned)(kv.n_pages * kv.page)) {
+            for (int e = threadIdx.x * VEC; e < 2 * kvn; e += 128 * VEC)
+                *reinterpret_cast<uint4*>((e < kvn ? kc + e : vc + (e - kvn)) + (size_t)slot * kvn) =
+                    *reinterpret_cast<const uint4*>(qkv + (size_t)row * Nqkv + (size_t)H * HD + e);
+        } else if (slot >= 0 && threadIdx.x == 0) {
+            set_status(status, ST_BAD_PAGE);
+        }
+    }
+    const int32_t* cu = kv.cu_rows;
     for (int c = threadIdx.x; c < HD; c += blockDim.x) sq[c] = tof(qkv[(size_t)row * Nqkv + (size_t)h * HD + c]) * scale_log2;
-    __syncthreads();
-    const int r = s_r;
-    if (r < 0) return;  // a row behind the last sequence stays as it was
-    const int len = kv.kv_len[r] - (kv.cu_rows[r + 1] - row) + 1;  // keys that the row sees
-    if (kv.kv_len[r] > (long long)kv.max_blocks * kv.page || len <= 0) {
+    if (row < cu[0] || row >= cu[kv.n_req]) return;  // behind the last sequence: stays as it was
+    const int r = row_request_warp(cu, kv.n_req, row, lane);
+    const int lo = cu[r], hi = cu[r + 1], all = kv.kv_len[r];
+    const int before = all - (hi - lo);  // positions in the cache
+    if (lo < 0 || hi > rows || before < 0 || all > (long long)kv.max_blocks * kv.page) {
         if (threadIdx.x == 0 && h == 0) set_status(status, ST_BAD_LENGTH);
         return;
     }
+    __syncthreads();
+    const int len = before + (row - lo) + 1;  // keys that the row sees
     const int32_t* table = kv.table + (size_t)r * kv.max_blocks;
-    const int shift = 31 - __clz(kv.page);
-    const int g = h / (H / nkv);
-    const size_t ld = (size_t)nkv * HD;
+    const int shift = 31 - __clz(kv.page), g = h / (H / nkv);
     float acc[EPL], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
     for (int j0 = warp * 32; j0 < len; j0 += 128) {
         const int j = j0 + lane;
-        int slot = -1;
-        if (j < len) {
+        const A *kr = nullptr, *vr = nullptr;  // null: a position without a page, which reads as zeros
+        if (j >= before && j < len) {
+            kr = qkv + (size_t)(lo + j - before) * Nqkv + (size_t)(H + g) * HD;
+            vr = kr + kvn;
+        } else if (j < len) {
             const int page = table[j >> shift];
-            if ((unsigned)page < (unsigned)kv.n_pages) slot = (page << shift) + (j & (kv.page - 1));
-            else set_status(status, ST_BAD_PAGE);
+            if ((unsigned)page < (unsigned)kv.n_pages) {
+                const size_t at = ((size_t)(page << shift) + (j & (kv.page - 1))) * kvn + (size_t)g * HD;
+                kr = kc + at;
+                vr = vc + at;
+            } else {
+                set_status(status, ST_BAD_PAGE);
+            }
         }
-        float sc = j < len ? 0.f : -INFINITY;  // a position without a page reads as zeros
-        if (slot >= 0) {
-            const A* kr = kc + (size_t)slot * ld + (size_t)g * HD;
+        float sc = j < len ? 0.f : -INFINITY;
+        if (kr) {
 #pragma unroll
             for (int c = 0; c < HD; c += VEC) {
                 float x[VEC];
@@ -393,17 +427,18 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restric
         for (int i = 0; i < EPL; ++i) acc[i] *= alpha;
         m = mn;
         const int n = min(32, len - j0);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float pk = __shfl_sync(0xffffffffu, pj, k);
-            const int sk = __shfl_sync(0xffffffffu, slot, k);
-            if (sk < 0) continue;
-            const A* vr = vc + (size_t)sk * ld + (size_t)g * HD;
+#pragma unroll 8
+        for (int k = 0; k < n; k += WAYS) {
+            const int key = k + (WAYS > 1 ? lane / HD : 0);  // below 32; a key behind the last weighs nothing
+            const float pk = __shfl_sync(0xffffffffu, pj, key);
+            const A* from = reinterpret_cast<const A*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vr), key));
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
-                if (lane + 32 * i < HD) acc[i] = fmaf(pk, tof(vr[lane + 32 * i]), acc[i]);
+                if (from) acc[i] = fmaf(pk, tof(from[WAYS > 1 ? lane % HD : lane + 32 * i]), acc[i]);
         }
     }
+#pragma unroll
+    for (int x = HD; x < 32; x <<= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], x);
     l = warp_sum(l);
     if (lane == 0) { sm[warp] = m; sl[warp] = l; }
 #pragma unroll
@@ -417,7 +452,7 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restric
         w4[w] = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - M);
         L += sl[w] * w4[w];
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;  // a row without a key gives zeros
+    const float inv = 1.f / L;
     for (int c = threadIdx.x; c < HD; c += blockDim.x) {
         float x = 0.f;
 #pragma unroll
@@ -505,19 +540,17 @@ void reorder_launch(const ReorderArgs& a, dim3 grid, cudaStream_t s) {
 }
 
 template <typename A>
-cudaError_t attention_simt_t(const void* qkv, int H, int nkv, int hd, int rows, const PagedKv& kv, void* o,
-                             int* status, cudaStream_t s) {
+cudaError_t attention_simt_t(const void* qkv, int H, int nkv, int hd, int rows, const int32_t* slots, const PagedKv& kv,
+                             void* o, int* status, cudaStream_t s) {
     const float sl = 1.44269504088896340736f / sqrtf((float)hd);
     const dim3 grid(rows, H);
     const A* q = reinterpret_cast<const A*>(qkv);
-    const A* k = reinterpret_cast<const A*>(kv.k);
-    const A* v = reinterpret_cast<const A*>(kv.v);
     A* out = reinterpret_cast<A*>(o);
     switch (hd) {
-        case 16: paged_attention_kernel<A, 16><<<grid, 128, 0, s>>>(q, H, nkv, k, v, kv, sl, out, status); break;
-        case 32: paged_attention_kernel<A, 32><<<grid, 128, 0, s>>>(q, H, nkv, k, v, kv, sl, out, status); break;
-        case 64: paged_attention_kernel<A, 64><<<grid, 128, 0, s>>>(q, H, nkv, k, v, kv, sl, out, status); break;
-        case 128: paged_attention_kernel<A, 128><<<grid, 128, 0, s>>>(q, H, nkv, k, v, kv, sl, out, status); break;
+        case 16: paged_attention_kernel<A, 16><<<grid, 128, 0, s>>>(q, H, nkv, rows, slots, kv, sl, out, status); break;
+        case 32: paged_attention_kernel<A, 32><<<grid, 128, 0, s>>>(q, H, nkv, rows, slots, kv, sl, out, status); break;
+        case 64: paged_attention_kernel<A, 64><<<grid, 128, 0, s>>>(q, H, nkv, rows, slots, kv, sl, out, status); break;
+        case 128: paged_attention_kernel<A, 128><<<grid, 128, 0, s>>>(q, H, nkv, rows, slots, kv, sl, out, status); break;
         default: return cudaErrorInvalidValue;
     }
     count_launch();
@@ -572,10 +605,10 @@ cudaError_t launch_paged_append(DType at, const void* qkv, int H, int nkv, int h
     return cudaGetLastError();
 }
 
-cudaError_t launch_paged_attention_simt(DType at, const void* qkv, int H, int nkv, int hd, int rows, const PagedKv& kv,
-                                        void* o, int* status, cudaStream_t s) {
-    return at == DT_BF16 ? attention_simt_t<bf16>(qkv, H, nkv, hd, rows, kv, o, status, s)
-                         : attention_simt_t<float>(qkv, H, nkv, hd, rows, kv, o, status, s);
+cudaError_t launch_paged_attention_simt(DType at, const void* qkv, int H, int nkv, int hd, int rows, const int32_t* slots,
+                                        const PagedKv& kv, void* o, int* status, cudaStream_t s) {
+    return at == DT_BF16 ? attention_simt_t<bf16>(qkv, H, nkv, hd, rows, slots, kv, o, status, s)
+                         : attention_simt_t<float>(qkv, H, nkv, hd, rows, slots, kv, o, status, s);
 }
 
 cudaError_t launch_last_rows(DType at, const void* x, int d, int rows, const int32_t* cu_rows, int n_req, void* out,

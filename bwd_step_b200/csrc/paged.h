@@ -35,9 +35,10 @@ cudaError_t launch_page_plan(int n_req, int page, int max_blocks, int n_pages, i
 cudaError_t launch_paged_append(DType at, const void* qkv, int H, int nkv, int hd, int rows, const int32_t* slots,
                                 const PagedKv& kv, int* status, cudaStream_t s);
 
-// o[row, h] = softmax over the keys at positions 0..pos(row) of the row's request, plain FMA kernel.
-cudaError_t launch_paged_attention_simt(DType at, const void* qkv, int H, int nkv, int hd, int rows, const PagedKv& kv,
-                                        void* o, int* status, cudaStream_t s);
+// The rows' k, v to their slots and o[row, h] = softmax over the keys at positions 0..pos(row) of the
+// row's request, plain FMA kernel.
+cudaError_t launch_paged_attention_simt(DType at, const void* qkv, int H, int nkv, int hd, int rows, const int32_t* slots,
+                                        const PagedKv& kv, void* o, int* status, cudaStream_t s);
 
 // The last new row of every request: out[r] = x[cu_rows[r + 1] - 1] (rows of d elements), zeros for a
 // request without new rows.

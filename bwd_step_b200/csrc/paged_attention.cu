@@ -1330,9 +1330,7 @@ cudaError_t paged_attention(DType at, const void* qkv, int H, int nkv, int hd, i
         return f(reinterpret_cast<const bf16*>(qkv), H, nkv, rows, max_new, slots, kv, reinterpret_cast<bf16*>(o), (char*)workspace,
                  status, s);
     }
-    cudaError_t e = launch_paged_append(at, qkv, H, nkv, hd, rows, slots, kv, status, s);
-    if (e != cudaSuccess) return e;
-    return launch_paged_attention_simt(at, qkv, H, nkv, hd, rows, kv, o, status, s);
+    return launch_paged_attention_simt(at, qkv, H, nkv, hd, rows, slots, kv, o, status, s);
 }
 
 }  // namespace nc
