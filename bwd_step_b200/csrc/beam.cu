@@ -95,7 +95,8 @@ struct Shared {
     uint8_t stage[kStages][kChunk];
     u64 score[kCand], key[kCand];  // the first block's: the gathered candidates
     int beam[kCand];
-    int count;
+    int count, pushed;        // candidates gathered; those that this block gave
+    int pushes[kCluster];     // what every block gave
     float sum[kMaxBeams], mx[kMaxBeams];       // this slice's maximum, and sum of exp(z - mx)
     double lse[kMaxBeams];
     uint32_t least[kMaxBeams];
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads + 32, 4) beam_select_kernel(const A* 
         if (lane == 0) {
             sh.n_active = __popc(m);
             sh.abort_flag = 0;
-            sh.count = 0;
+            sh.count = sh.pushed = 0;
             tc::fence_barrier_init();
         }
     }
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(kThreads + 32, 4) beam_select_kernel(const A* 
     }
     __syncthreads();
     auto push = [&](double v, u64 key, int k) {
+        atomicAdd(&sh.pushed, 1);
         const int to = atomicAdd(&first->count, 1);
         if (to < kCand) { first->score[to] = ordered(v); first->key[to] = key; first->beam[to] = k; }
     };
@@ -343,6 +345,8 @@ __global__ void __launch_bounds__(kThreads + 32, 4) beam_select_kernel(const A* 
         }
     }
     if (rank == 0 && tid < K && sh.finished[tid] && (double)sh.s0[tid] >= bound) push((double)sh.s0[tid], make_key(1u, a.eos), tid);
+    __syncthreads();
+    if (tid < S) cluster.map_shared_rank(&sh, tid)->pushes[rank] = sh.pushed;
     cluster.sync();
     // ---------------- 4: the candidates in their order
     auto put = [&](int i, u64 score, u64 key, int beam) {
@@ -352,20 +356,18 @@ __global__ void __launch_bounds__(kThreads + 32, 4) beam_select_kernel(const A* 
         a.parents[to] = beam;
         if (a.finished_out) a.finished_out[to] = sh.finished[beam] || token == a.eos;
     };
-    const int c = first->count;
-    if (c >= K && c <= kCand) {
-        if (rank == 0 && tid < c) {
-            const u64 sc = sh.score[tid], ke = sh.key[tid];
-            const int be = sh.beam[tid];
-            int above = 0;
-#pragma unroll 4
-            for (int i = 0; i < c; ++i) {
-                const u64 x = sh.score[i];
-                above += x > sc;
-                if (x == sc && i != tid) above += better(x, sh.beam[i], sh.key[i], sc, be, ke);
+    int c = 0;
+    for (int s = 0; s < S; ++s) c += sh.pushes[s];
+    if (c >= K && c <= kCand) {  // no block reads another's memory from here on
+        if (rank == 0)
+            for (int i = warp; i < c; i += kWarps + 1) {  // a warp to a candidate, the better ones counted by the lanes
+                const u64 sc = sh.score[i], ke = sh.key[i];
+                const int be = sh.beam[i];
+                int above = 0;
+                for (int o = lane; o - lane < c; o += 32)
+                    above += __popc(__ballot_sync(0xffffffffu, o < c && better(sh.score[o], sh.beam[o], sh.key[o], sc, be, ke)));
+                if (lane == 0 && above < K) put(above, sc, ke, be);
             }
-            if (above < K) put(above, sc, ke, be);
-        }
     } else {
         // Too many alike, or too few of finite score: K times the best candidate behind the last one, each
         // block's threads over their own values, the blocks' bests through distributed shared memory.
@@ -409,8 +411,8 @@ __global__ void __launch_bounds__(kThreads + 32, 4) beam_select_kernel(const A* 
             if (rank == 0 && tid == 0) put(i, bs, bk, bb);
             last_s = bs; last_k = bk; last_b = bb;
         }
+        cluster.sync();  // every block's shared memory has been read
     }
-    cluster.sync();  // every block's shared memory has been read
 }
 
 template <typename A>

@@ -109,7 +109,7 @@ int nc_beam_reorder(nc_model* m, void* kv_cache, int batch, int beams, int T_max
     if (!m || !on_model_device(m) || batch < 1 || beams < 1 || T_max < 1) return NC_ERR_INVALID_ARG;
     if (!kv_cache || !al16(kv_cache) || !all4({parents}) || start < 0 || end < start || end > T_max)
         return NC_ERR_INVALID_ARG;
-    if (beams > NC_MAX_BEAMS || batch > (1 << 20)) return NC_ERR_UNSUPPORTED_SHAPE;
+    if (beams > NC_MAX_BEAMS || batch > (1 << 20) || 2ll * m->L * batch > (1 << 30)) return NC_ERR_UNSUPPORTED_SHAPE;
     ReorderArgs a{};
     a.base = (char*)kv_cache;
     a.planes = 2 * m->L; a.batch = batch; a.beams = beams;
@@ -128,7 +128,7 @@ int nc_beam_reorder_paged(nc_model* m, void* kv_pages, int batch, int beams, int
     if (!kv_pages || !al16(kv_pages) || !all4({parents, block_table, starts, ends})) return NC_ERR_INVALID_ARG;
     const int r = check_paging(page_size, max_blocks, n_pages);
     if (r != NC_OK) return r;
-    if (beams > NC_MAX_BEAMS || batch > (1 << 20)) return NC_ERR_UNSUPPORTED_SHAPE;
+    if (beams > NC_MAX_BEAMS || batch > (1 << 20) || 2ll * m->L * batch > (1 << 30)) return NC_ERR_UNSUPPORTED_SHAPE;
     ReorderArgs a{};
     a.base = (char*)kv_pages;
     a.planes = 2 * m->L; a.batch = batch; a.beams = beams;

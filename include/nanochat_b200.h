@@ -269,9 +269,10 @@ int nc_page_plan(nc_model* m, int n_req, int page_size, int max_blocks, int n_pa
  *   qkv: device [rows, (n_head + 2 n_kv_head) head_dim], packed rows as the fused
  *     projection leaves them after QK-norm and RoPE; cu_rows, kv_len, slots as
  *     nc_page_plan writes them.
- *   First the k, v heads of every row are written to its slot (rows with slot
- *   < 0 have none), then row i of request r, at position
- *   p = kv_len[r] - cu_rows[r + 1] + i, attends to positions 0..p:
+ *   The k, v heads of every row are written to its slot (rows with slot < 0 have
+ *   none; a request's rows have the slots of their positions), and row i of
+ *   request r, at position p = kv_len[r] - cu_rows[r + 1] + i, attends to
+ *   positions 0..p, the step's own among them:
  *   o[i] = softmax(q K^T / sqrt(head_dim)) V into o [rows, n_head head_dim].
  *   Rows from cu_rows[n_req] on are left as they were.
  *   max_new: an upper bound of every request's number of new rows, 0 if none is
@@ -279,11 +280,14 @@ int nc_page_plan(nc_model* m, int n_req, int page_size, int max_blocks, int n_pa
  *   reported as NC_ERR_BAD_LENGTH and may be left without output, as is one whose
  *   length or rows do not fit the table or the step.
  *   workspace: nc_paged_attention_workspace_bytes(m, n_req, rows) bytes,
- *   256-byte aligned; contents on entry are ignored.
+ *   256-byte aligned; contents on entry are ignored.  It serves one call at a time:
+ *   calls that may run at once (two streams, two graphs) need one each.
  * A block without a page inside a request's length reads as zeros and is
  * reported as NC_ERR_BAD_PAGE.  Cache contents past a request's length are not
  * used, whatever they are.  Results are bitwise reproducible for the same
- * lengths. */
+ * lengths, table width and max_new.  bf16 models with head_dim 64 or 128 and at
+ * most 128 query heads per K/V head run on the tensor cores (requests with one new
+ * row and at most 16 such heads on a kernel of their own), others on plain FMAs. */
 size_t nc_paged_attention_workspace_bytes(const nc_model* m, int n_req, int rows);
 int nc_paged_attention(nc_model* m, const void* qkv, int rows, int n_req, int max_new, const int32_t* cu_rows,
                        const int32_t* kv_len, const int32_t* slots, const int32_t* block_table, int max_blocks,

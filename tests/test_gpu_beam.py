@@ -141,6 +141,31 @@ def test_select_infinities_and_nan():
     _check(z, s, "fp32")
 
 
+@pytest.mark.parametrize("k,v", [(8, 65536), (32, 65536), (32, 512), (5, 2112)])
+def test_select_with_few_ids_allowed(k, v):
+    """All ids but a few masked: fewer candidates of finite score than lanes, than beams, one, none."""
+    z, s = _random(4, k, v, k)
+    for b, allowed in enumerate((40, 3, 1, 0)):
+        mask = torch.ones(v, dtype=torch.bool)
+        mask[torch.randperm(v, generator=torch.Generator().manual_seed(b))[:allowed]] = False
+        z[b, :, mask] = -float("inf")
+    _check(z, s, "bf16")
+    s[:, 1:] = -float("inf")  # and a search's first step
+    _check(z, s, "bf16")
+
+
+@pytest.mark.parametrize("k,v", [(1, 65536), (32, 65536), (16, 320)])
+def test_select_of_equal_logits(k, v):
+    _check(torch.full((2, k, v), 1.5), torch.linspace(0, -2, 2 * k).view(2, k), "bf16")
+
+
+def test_select_of_a_large_vocabulary():
+    """Several chunks of logits in a block."""
+    z, s = _random(2, 3, 64 * 4100, 17)
+    _check(z, s, "bf16")
+    _check(z, s, "fp32")
+
+
 def test_select_refusals():
     m = _model(512)
     z = torch.zeros(2, 3, 512, dtype=torch.bfloat16, device="cuda")
@@ -229,6 +254,50 @@ def test_search_over_the_dense_cache():
         want, ws_ = _oracle_search(cfg, w, prompts[i].tolist(), k, steps, -1)
         assert seqs[i] == want
         assert np.allclose(scores[i].cpu().numpy(), ws_, atol=1e-3)
+
+
+def test_a_captured_step_of_a_search():
+    """Selection, planning, reordering and the model's forward in one graph, replayed, against the same calls made singly."""
+    from bwd_step_b200.generate import PagedCache
+    cfg = _cfg(head_dim=64)
+    bits, w = synth.make_weights(cfg, seed=2, dtype="bf16", std=0.3)
+    W = to_device_weights(bits, w, "bf16")
+    m = Model(cfg.as_dict(), "bf16")
+    b, k, n = 2, 3, 19
+    prompts = torch.from_numpy(np.random.default_rng(0).integers(0, cfg.vocab, (b, 1, n)).astype(np.int32)).cuda()
+
+    def begin():
+        c = PagedCache(m, 40, 16, b * k, 64, b * k * n)
+        c.plan(torch.full((b * k,), n, dtype=torch.int32, device="cuda"), b * k * n)
+        s = dict(cache=c, logits=torch.empty(b * k, cfg.vocab, dtype=torch.bfloat16, device="cuda"),
+                 scores=torch.tensor([[0.0, -1.0, -2.0]] * b, device="cuda"),
+                 tok=torch.empty(b, k, dtype=torch.int32, device="cuda"), par=torch.empty(b, k, dtype=torch.int32, device="cuda"),
+                 start=torch.full((b * k,), n, dtype=torch.int32, device="cuda"), end=torch.zeros(b * k, dtype=torch.int32, device="cuda"),
+                 one=torch.ones(b * k, dtype=torch.int32, device="cuda"))
+        c.forward(prompts.expand(b, k, n).reshape(-1).contiguous(), W, s["logits"], max_new=n)
+        return s
+
+    def step(s):
+        c = s["cache"]
+        m.beam_select(s["logits"], s["scores"], s["scores"], s["tok"], s["par"])
+        s["end"].copy_(c.kv_len)
+        c.plan(s["one"], b * k)
+        m.beam_reorder_paged(c.kv, s["par"], c.block_table, s["start"], s["end"])
+        c.forward(s["tok"].view(-1), W, s["logits"], max_new=1)
+    one, two = begin(), begin()
+    seen = []
+    for _ in range(6):
+        step(one)
+        seen.append((one["tok"].clone(), one["par"].clone(), one["scores"].clone(), one["logits"].clone()))
+    step(two)  # the first step outside, as a warm-up
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(two)
+    for tok, par, scores, logits in seen[1:]:
+        g.replay()
+        assert torch.equal(two["tok"], tok) and torch.equal(two["par"], par)
+        assert torch.equal(two["scores"], scores) and torch.equal(two["logits"], logits)
+    assert m.check() == 0
 
 
 @pytest.mark.parametrize("precision,hd,h,nkv", [("bf16", 128, 2, 1), ("bf16", 64, 4, 1), ("bf16", 16, 4, 1), ("fp32", 32, 4, 2)])

@@ -339,6 +339,65 @@ def test_a_captured_step_follows_new_lengths(lens, longer):
     assert m.check() == 0
 
 
+def test_attention_over_many_requests():
+    """As many requests as one call takes, one new token or a few, short and empty ones among them."""
+    rng = random.Random(3)
+    lens = [(rng.choice([0, 1, 15, 40]), rng.choice([0, 1, 1, 1, 3])) for _ in range(4095)] + [(300, 9)]
+    _check(Step(1, 1, 64, 16, lens, seed=5), _model(1, 1, 64), "bf16")
+
+
+@pytest.mark.parametrize("lens", [[(500, 1), (70, 1)], [(500, 30), (70, 2)]])
+def test_attention_at_slots_far_into_a_large_cache(lens):
+    """Pages behind the 4 GiB that 32-bit byte offsets reach."""
+    m, s = _model(), Step(10, 1, 128, 256, lens, seed=12)
+    want = s.run(m).clone()
+    t = Step(10, 1, 128, 256, lens, seed=12)
+    far = 70000
+    k, v = (torch.empty(far + x.shape[0], 256, 1, 128, dtype=torch.bfloat16, device="cuda") for x in (t.k, t.v))
+    k[far:], v[far:] = t.k, t.v
+    t.k, t.v = k, v
+    t.table[t.table >= 0] += far
+    t.slots[t.slots >= 0] += far * 256
+    assert torch.equal(t.run(m), want) and m.check() == 0
+    at = s.slots.long()
+    assert torch.equal(k.view(-1, 128)[at + far * 256], s.k.view(-1, 128)[at])
+
+
+def test_requests_may_share_the_pages_of_a_common_prefix():
+    m = _model()
+    s = Step(10, 1, 128, 16, [(64, 1), (64, 20), (80, 1)], seed=15)
+    for r in (1, 2):  # the first four pages are the first request's
+        s.tables[r][:4] = s.tables[0][:4]
+    s.table[:, :4] = s.table[0, :4]
+    _check(s, m, "bf16")
+
+
+def test_calls_at_once_on_two_streams():
+    """Two steps of one model on two streams, each with its own arrays and workspace."""
+    m = _model()
+    steps = [Step(10, 1, 128, 16, lens, seed=7) for lens in (CHUNKS, DECODE) for _ in range(4)]
+    want = [Step(10, 1, 128, 16, s.lens, seed=7).run(m).clone() for s in steps]
+    ws = [torch.empty(m.paged_attention_workspace_bytes(len(s.lens), s.rows), dtype=torch.uint8, device="cuda") for s in steps]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i, s in enumerate(steps):
+        m.paged_attention(s.qkv, s.cu, s.kv_len, s.slots, s.table, s.k, s.v, s.o, ws[i], max_new=max(n for _, n in s.lens),
+                          stream=streams[i % 2])
+    torch.cuda.synchronize()
+    assert m.check() == 0
+    for s, w in zip(steps, want):
+        assert torch.equal(s.o, w)
+
+
+@pytest.mark.parametrize("h,hd", [(10, 128), (4, 16)])
+def test_a_request_with_more_rows_than_max_new_is_reported(h, hd):
+    m = _model(h, 1, hd)
+    s = Step(h, 1, hd, 16, [(100, 1), (50, 3)], seed=1)
+    s.run(m, max_new=1)
+    # the plain kernel computes it all the same
+    assert m.check() == (_lib.NC_ERR_BAD_LENGTH if hd == 128 else 0)
+
+
 def test_attention_reports_missing_pages_and_lengths():
     m = _model()
     s = Step(10, 1, 128, 16, [(100, 1), (50, 1)], seed=1)
