@@ -23,6 +23,11 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 64;        // keys of a decode tile
+// Where the table has no more positions than this, nothing is cut over blocks and there is nothing to
+// join.  Steps with chunks: 8 prompts of some 225 rows on up to 700 positions take 30.1 us instead of
+// 34.8.  Steps of decoding requests alone, whose join is most of what they do: four requests of up to
+// 700 positions take 12.4 us whole and 10.3 cut, so only tables of a few tiles.
+constexpr int kWholePositions = 1024, kWholeDecoding = 256;
 constexpr int kDecRows = 16;     // query heads of a K/V head that the decode kernel takes
 constexpr int kDecThreads = 320; // 8 consumer warps, the producer, and one that writes the cache
 constexpr float kLog2eF = 1.44269504088896340736f;
@@ -43,6 +48,7 @@ struct DecodeArgs {
     bf16* o;
     Partials part;
     int H, nkv, Hg, rows, piece, max_new;  // piece: rows of one copy, min(page, kTile)
+    bool whole;                            // no (request, K/V head) is cut
     float scale_log2;
     int* status;
 };
@@ -229,7 +235,13 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     });
     const int W = pre[a.kv.n_req], G = max(1, min((int)gridDim.x, W));  // no block between two others is empty
     const bool busy = W > 0 && (int)blockIdx.x < G;
-    const int x0 = busy ? (int)cut(W, G, blockIdx.x) : 0, x1 = busy ? (int)cut(W, G, blockIdx.x + 1) : 0;
+    auto edge = [&](int c) {  // first tile of block c
+        const int x = (int)cut(W, G, c);
+        if (!a.whole || x >= W) return x;
+        const DecSeg s = dec_seg(a, pre, x, W);
+        return s.k0 ? x - s.k0 + s.tiles : x;
+    };
+    const int x0 = busy ? edge(blockIdx.x) : 0, x1 = busy ? edge(blockIdx.x + 1) : 0;
     const int pshift = 31 - __clz(a.piece), shift = 31 - __clz(a.kv.page);
 
     if (warp == 8) {
@@ -1277,13 +1289,15 @@ cudaError_t attention(const bf16* qkv, int H, int nkv, int rows, int max_new, co
     const int Hg = H / nkv, G = device_sm_count();
     const float scale_log2 = kLog2eF / sqrtf((float)HD);
     const bool decodes = Hg <= kDecRows, chunks = !decodes || max_new != 1;
+    const bool whole = (long long)kv.max_blocks * kv.page <= (chunks ? kWholePositions : kWholeDecoding);
+    static_assert(kWholePositions <= 128 * kWholeTiles, "the chunk kernel cuts nothing either");
     JoinSet jd{}, jc{};
     cudaError_t e;
     if (decodes) {
         if ((e = ensure_smem_limit((const void*)paged_decode_kernel<HD>, DecLayout<HD>::bytes(kMaxRequests))) != cudaSuccess) return e;
         jd = {partials(ws, G, kDecRows, HD), kDecRows, kDecRows, 1, (Hg + 1) / 2};
         ws += partial_bytes(G, kDecRows, HD);
-        DecodeArgs a{qkv, slots, kv, o, jd.part, H, nkv, Hg, rows, std::min(kv.page, kTile), max_new, scale_log2, status};
+        DecodeArgs a{qkv, slots, kv, o, jd.part, H, nkv, Hg, rows, std::min(kv.page, kTile), max_new, whole, scale_log2, status};
         CUtensorMap tk, tv;
         if (!map_pool(&tk, kv.k, nkv, HD, kv, a.piece) || !map_pool(&tv, kv.v, nkv, HD, kv, a.piece)) return cudaErrorUnknown;
         paged_decode_kernel<HD><<<G, kDecThreads, DecLayout<HD>::bytes(kv.n_req), s>>>(tk, tv, a);
@@ -1310,6 +1324,7 @@ cudaError_t attention(const bf16* qkv, int H, int nkv, int rows, int max_new, co
         e = launch_pdl((const void*)paged_chunk_kernel<HD>, dim3(G), kChunkThreads, ChunkLayout<HD>::bytes(kv.n_req), s, args);
         if (e != cudaSuccess) return e;
     }
+    if (whole) return cudaSuccess;
     void* args[] = {&jd, &jc, &H, const_cast<int*>(&Hg), &o};
     return launch_pdl((const void*)paged_join_kernel<HD>, dim3(G, jd.blocks + jc.blocks), 256, 0, s, args);
 }
