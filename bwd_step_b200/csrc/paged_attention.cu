@@ -7,7 +7,7 @@
 // each key and value is read once for all of them.  Bound by HBM.
 //
 // Work is cut evenly over the SMs: the requests' key tiles of all K/V heads form
-// one line, and block c of G takes the tiles [c W / G, (c + 1) W / G) of its W.
+// one line, whose W tiles are dealt out in order, W / G to each of G blocks.
 // A unit (a (request, K/V head), or a part of a chunk) that lies in one block is finished
 // there; one that is cut leaves a partial output, row maximum and sum in each of its
 // blocks, and a last kernel joins them in the blocks' order, so the result does not depend on timing.
@@ -137,8 +137,18 @@ __device__ __forceinline__ int find_request(const T* pre, int n, T x) {
     return lo;
 }
 
-__device__ __forceinline__ long long cut(long long W, int G, int c) { return W * c / G; }  // first tile of block c
-__device__ __forceinline__ int block_of(long long W, int G, long long x) { return (int)(((x + 1) * G - 1) / W); }
+// The line of W tiles cut over G blocks: the first W % G of them have one tile more.
+template <typename T>
+struct Cut {
+    T each;
+    int more;
+    __device__ __forceinline__ Cut(T W, int G) : each(W / (unsigned)G), more((int)(W - each * (unsigned)G)) {}
+    __device__ __forceinline__ T first(int c) const { return each * (unsigned)c + (unsigned)min(c, more); }  // tile of block c
+    __device__ __forceinline__ int block(T x) const {  // that has tile x
+        const T big = (each + 1) * (unsigned)more;
+        return x < big ? (int)(x / (each + 1)) : more + (int)((x - big) / each);
+    }
+};
 
 // ---------------------------------------------------------------- decode
 template <int HD>
@@ -235,8 +245,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     });
     const int W = pre[a.kv.n_req], G = max(1, min((int)gridDim.x, W));  // no block between two others is empty
     const bool busy = W > 0 && (int)blockIdx.x < G;
+    const Cut<unsigned> line((unsigned)W, G);
     auto edge = [&](int c) {  // first tile of block c
-        const int x = (int)cut(W, G, c);
+        const int x = (int)line.first(c);
         if (!a.whole || x >= W) return x;
         const DecSeg s = dec_seg(a, pre, x, W);
         return s.k0 ? x - s.k0 + s.tiles : x;
@@ -250,6 +261,20 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         bool ok = true;
         for (int x = x0; ok && x < x1; ++k) {
             const DecSeg s = dec_seg(a, pre, x, x1);
+            const int32_t* table = a.kv.table + (size_t)s.r * a.kv.max_blocks;
+            const int per = kTile >> pshift;  // pieces of a tile
+            int have, entry;                  // 32 pieces' slots in the lanes, from piece `have` on
+            auto entries = [&](int p0) {
+                have = p0;
+                const int pos = (p0 + lane) << pshift;
+                entry = a.kv.n_pages << shift;  // past the end: reads as zeros
+                if (pos < s.len) {
+                    const int page = table[pos >> shift];
+                    if ((unsigned)page < (unsigned)a.kv.n_pages) entry = (page << shift) + (pos & (a.kv.page - 1));
+                    else set_status(a.status, ST_BAD_PAGE);
+                }
+            };
+            entries(s.k0 * per);
             ok = warp_wait(q_empty + 8 * (k % Lay::QS), ((k / Lay::QS) & 1) ^ 1, abort_flag, a.status);
             if (!ok) break;
             if (lane == 0) {
@@ -261,21 +286,9 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 bulk_load(to + (kDecRows + 1) * HD * 2, from + (size_t)(a.H + a.nkv + s.g) * HD, HD * 2, bar);
             }
             __syncwarp();
-            const int32_t* table = a.kv.table + (size_t)s.r * a.kv.max_blocks;
-            const int per = kTile >> pshift;  // pieces of a tile
-            int have = -1, entry = 0;         // 32 pieces' slots in the lanes, from piece `have` on
             for (int kt = s.k0; kt < s.k1; ++kt, ++i) {
                 const int p0 = kt * per, np = min(per, (s.len - kt * kTile + a.piece - 1) >> pshift);
-                if (have < 0 || p0 + np > have + 32) {
-                    have = p0;
-                    const int pos = (p0 + lane) << pshift;
-                    entry = a.kv.n_pages << shift;  // past the end: reads as zeros
-                    if (pos < s.len) {
-                        const int page = table[pos >> shift];
-                        if ((unsigned)page < (unsigned)a.kv.n_pages) entry = (page << shift) + (pos & (a.kv.page - 1));
-                        else set_status(a.status, ST_BAD_PAGE);
-                    }
-                }
+                if (p0 + np > have + 32) entries(p0);
                 const int st = i % ST;
                 const uint32_t ph = (i / ST) & 1;
                 ok = warp_wait(empty + 8 * st, ph ^ 1, abort_flag, a.status);
@@ -334,7 +347,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 const DecSeg s = dec_seg(a, pre, x1 - 1, x1);  // the block's last (request, K/V head)
                 const long long end = s.unit + s.tiles;
                 if (s.unit >= x0 && end > x1)
-                    d = make_int4(s.row, s.g, 2 * (block_of(W, G, end - 1) - (int)blockIdx.x + 1) + (s.unit == x0 ? 0 : 1), 1);
+                    d = make_int4(s.row, s.g, 2 * (line.block((unsigned)(end - 1)) - (int)blockIdx.x + 1) + (s.unit == x0 ? 0 : 1), 1);
             }
             a.part.desc[blockIdx.x] = d;
         }
@@ -818,7 +831,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         if (threadIdx.x == 0) a.part.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
-    const long long x0 = cut(W, G, blockIdx.x), x1 = cut(W, G, blockIdx.x + 1);
+    const Cut<unsigned long long> line(W, G);
+    const long long x0 = line.first(blockIdx.x), x1 = line.first(blockIdx.x + 1);
     if (warp == 9) tmem_alloc(smem_u32(tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
@@ -976,7 +990,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (; w.x < w.x1; w.next(a)) {
             if (!w.whole && w.unit >= x0 && w.unit + w.tiles > x1)
                 d = make_int4(w.row + w.tok0, w.g,
-                              2 * (block_of(W, G, w.unit + w.tiles - 1) - (int)blockIdx.x + 1) + (w.unit == x0 ? 0 : 1), w.toks);
+                              2 * (line.block(w.unit + w.tiles - 1) - (int)blockIdx.x + 1) + (w.unit == x0 ? 0 : 1), w.toks);
             if (x == 1 && w.toks <= a.tt) continue;
             const bool live = in && x * a.tt + rt < w.toks;
             const int k0 = w.k0, k1 = w.k1;
