@@ -598,14 +598,11 @@ __device__ __forceinline__ long long floor_sum128(unsigned n, unsigned a, unsign
     return sum;
 }
 
-// Key tiles of the first b units of a request's chunk for one K/V head: the tiles up to each unit's last token.
-__device__ __forceinline__ long long unit_tiles(int n, int len, int unit, int b) {
-    const int full = min(b, (n - 1) / unit);  // all but the chunk's last unit end `unit` tokens further on
-    long long t = full > 0 ? floor_sum128(full, unit, len - n + unit + 127) : 0;
-    if (b > full) t += (len + 127) >> 7;
-    return t;
+// Key tiles of a request's chunk for one K/V head: over its units, the tiles up to each one's last token.
+__device__ __forceinline__ long long chunk_tiles(int n, int len, int unit) {
+    const int full = (n - 1) / unit;  // all but the chunk's last unit end `unit` tokens further on
+    return (full ? floor_sum128(full, unit, len - n + unit + 127) : 0) + ((len + 127) >> 7);
 }
-__device__ __forceinline__ long long chunk_tiles(int n, int len, int unit) { return unit_tiles(n, len, unit, (n + unit - 1) / unit); }
 
 __device__ __forceinline__ long long ChunkArgs::tiles(int r) const {
     int row, n, len;
@@ -649,17 +646,25 @@ struct ChunkWalk {
         request(a.kv, a.rows, r, row, n, len);
         g = (int)(rem / per);
         rem -= g * per;
-        // the last unit that begins no later: 32 ways at a time
-        int lo = 0, hi = (n + 2 * a.tt - 1) / (2 * a.tt);  // tiles before unit lo <= rem < those before hi
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, b1 = min(hi, lo + lane * step);
-            const unsigned ok = __ballot_sync(0xffffffffu, b1 < hi && unit_tiles(n, len, 2 * a.tt, b1) <= rem);
-            const int k = 31 - __clz(ok);  // lane 0's is always
-            hi = min(hi, lo + (k + 1) * step);
-            lo += k * step;
+        // the unit that has tile rem, 32 units at a time
+        for (b = 0;; b += 32) {
+            const int e = min(n, (b + lane + 1) * 2 * a.tt);
+            const int mine = (b + lane) * 2 * a.tt < n ? (len - n + e + 127) >> 7 : 0;
+            long long t = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, t, o);
+                if (lane >= o) t += y;
+            }
+            const unsigned in = __ballot_sync(0xffffffffu, rem < t);
+            if (in) {
+                const int at = __ffs(in) - 1;
+                rem -= __shfl_sync(0xffffffffu, t - mine, at);
+                b += at;
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, t, 31);
         }
-        b = lo;
-        rem -= unit_tiles(n, len, 2 * a.tt, b);
         set(a);
         k0 = (int)rem;
         unit = x - k0;
@@ -1113,34 +1118,30 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             char* const mine = whole ? reinterpret_cast<char*>(a.o + (size_t)(w.row + w.tok0 + x * a.tt + rt) * a.H * HD + (size_t)(w.g * a.Hg + r % a.Hg) * HD)
                                      : reinterpret_cast<char*>(a.part.o + at * HD);
             const unsigned lives = __ballot_sync(0xffffffffu, live);
-            const int lines = HD * (whole ? 2 : 4) / 128;
+            // (little code: it runs once a piece, from a cold instruction cache)
 #pragma unroll 1
-            for (int c = 0; c < lines; ++c) {
+            for (int t = 0; t < HD / 32; ++t) {  // 32 columns: a line of the workspace, half a line of o
+                float o[32];
+                tmem_ld32(tO + 32 * t, o);
                 if (whole) {
 #pragma unroll
-                    for (int hk = 0; hk < 2; ++hk) {
-                        float o[32];
-                        tmem_ld32(tO + 64 * c + 32 * hk, o);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            pass[lane * 8 + ((4 * hk + i) ^ (lane & 7))] =
-                                make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv), pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                           pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        pass[lane * 8 + ((4 * (t & 1) + i) ^ (lane & 7))] =
+                            make_uint4(pack2(o[8 * i] * inv, o[8 * i + 1] * inv), pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                       pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    if (!(t & 1)) continue;
                 } else {
-                    uint32_t o[32];
-                    tmem_ld32_issue(tO + 32 * c, o);
-                    tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        pass[lane * 8 + (i ^ (lane & 7))] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        *reinterpret_cast<float4*>(&pass[lane * 8 + (i ^ (lane & 7))]) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
                 __syncwarp();
-#pragma unroll
+                const int off = 128 * (whole ? t >> 1 : t) + 16 * (lane & 7);
+#pragma unroll 2
                 for (int i = 0; i < 8; ++i) {
                     const int row = 4 * i + (lane >> 3);
                     char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), row));
-                    if (lives >> row & 1) *reinterpret_cast<uint4*>(to + 128 * c + 16 * (lane & 7)) = pass[row * 8 + ((lane & 7) ^ (row & 7))];
+                    if (lives >> row & 1) *reinterpret_cast<uint4*>(to + off) = pass[row * 8 + ((lane & 7) ^ (row & 7))];
                 }
                 __syncwarp();
             }
