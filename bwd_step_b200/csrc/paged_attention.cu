@@ -16,7 +16,6 @@
 #include "tc_common.cuh"
 #include <cudaTypedefs.h>
 #include <algorithm>
-#include <type_traits>
 
 namespace nc {
 namespace {
@@ -544,7 +543,6 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 constexpr int kChunkThreads = 320;  // softmax of half a, of half b (a warpgroup each); producer, MMA, two idle warps
 constexpr int kChunkRows = 256;
 constexpr int kWholeTiles = 10;  // units of so many key tiles are not cut: 8 requests of some 900 positions 33.9 -> 30.5 us
-constexpr int kPolyPairs = 1;  // pairs of scores, of every eight, that take 2^x from the FMA pipe
 
 struct ChunkArgs {
     PagedKv kv;
@@ -702,25 +700,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(taddr));
     tmem_wait_ld();
-}
-
-// 2^x of two values on the FMA pipe, as in the training attention: x = n + f, 2^f by a cubic
-// fitted on [-1/2, 1/2] (maximum relative error 7.5e-5, below the rounding of P to bf16), n
-// added to the exponent field.
-__device__ __forceinline__ void exp2_fma(uint64_t x, float& e0, float& e1) {
-    const uint64_t shift = f2_pack(12582912.f, 12582912.f), back = f2_pack(-12582912.f, -12582912.f);
-    float x0, x1, t0, t1, p0, p1;
-    f2_unpack(x, x0, x1);
-    x = f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-    const uint64_t t = f2_add(x, shift), n = f2_add(t, back);
-    const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), x);
-    uint64_t p = f2_fma(f2_pack(0.0551716685f, 0.0551716685f), f, f2_pack(0.2426111251f, 0.2426111251f));
-    p = f2_fma(p, f, f2_pack(0.6932609677f, 0.6932609677f));
-    p = f2_fma(p, f, f2_pack(0.9999280572f, 0.9999280572f));
-    f2_unpack(t, t0, t1);
-    f2_unpack(p, p0, p1);
-    e0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-    e1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 
 // The one thread of the warp that issues its products.  Chosen by elect.sync, not by its lane, so that
@@ -1033,14 +1012,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int k = 0; k < 4; ++k) mx4[k] = -INFINITY;
                 if (diag) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 2)
-                        mx4[(c >> 1) & 3] = max3f(mx4[(c >> 1) & 3], c > lim ? -INFINITY : __uint_as_float(sr[c]),
-                                                  c + 1 > lim ? -INFINITY : __uint_as_float(sr[c + 1]));
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 128; c += 2)
-                        mx4[(c >> 1) & 3] = max3f(mx4[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                    for (int c = 0; c < 128; ++c)
+                        if (c > lim) sr[c] = 0xff800000u;  // -inf
                 }
+#pragma unroll
+                for (int c = 0; c < 128; c += 2)
+                    mx4[(c >> 1) & 3] = max3f(mx4[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
                 float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                 mx *= a.scale_log2;
                 const bool rescale = live && mx > m + 8.f;  // rows of nothing hold anything
@@ -1063,43 +1040,29 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
                 // P = 2^(s * scale - mu) as packed bf16 over the score columns, 64 keys handed over at a time
-                auto exp_pack = [&](auto poly) {
-                    constexpr bool kPoly = decltype(poly)::value;
 #pragma unroll
-                    for (int hk = 0; hk < 2; ++hk) {
+                for (int hk = 0; hk < 2; ++hk) {
 #pragma unroll
-                        for (int q8 = 4 * hk; q8 < 4 * hk + 4; ++q8) {
-                            uint32_t pk[8];
+                    for (int q8 = 4 * hk; q8 < 4 * hk + 4; ++q8) {
+                        uint32_t pk[8];
 #pragma unroll
-                            for (int c = 0; c < 16; c += 2) {
-                                const int cc = 16 * q8 + c;
-                                const uint64_t y = f2_fma(f2_pack(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, nmu2);
-                                float e0, e1;
-                                if (kPoly && (c / 2) * kPolyPairs % 8 < kPolyPairs) {
-                                    exp2_fma(y, e0, e1);
-                                } else {
-                                    float y0, y1;
-                                    f2_unpack(y, y0, y1);
-                                    if (!kPoly && diag) {
-                                        if (cc > lim) y0 = -INFINITY;
-                                        if (cc + 1 > lim) y1 = -INFINITY;
-                                    }
-                                    e0 = ex2(y0);
-                                    e1 = ex2(y1);
-                                }
-                                sum2[(c >> 1) & 1] = f2_add(sum2[(c >> 1) & 1], f2_pack(e0, e1));
-                                pk[c >> 1] = pack2(e0, e1);
-                            }
-                            tmem_st8_nowait(tS + 8 * q8, pk);
+                        for (int c = 0; c < 16; c += 2) {
+                            const int cc = 16 * q8 + c;
+                            const uint64_t y = f2_fma(f2_pack(__uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1])), sc2, nmu2);
+                            float e0, e1;
+                            f2_unpack(y, e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            sum2[(c >> 1) & 1] = f2_add(sum2[(c >> 1) & 1], f2_pack(e0, e1));
+                            pk[c >> 1] = pack2(e0, e1);
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(p_full + 16 * x + 8 * hk);
+                        tmem_st8_nowait(tS + 8 * q8, pk);
                     }
-                };
-                if (!diag) exp_pack(std::true_type{});
-                else exp_pack(std::false_type{});
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full + 16 * x + 8 * hk);
+                }
                 float s00, s01, s10, s11;
                 f2_unpack(sum2[0], s00, s01);
                 f2_unpack(sum2[1], s10, s11);
