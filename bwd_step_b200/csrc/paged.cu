@@ -9,6 +9,7 @@
 #include "common.cuh"
 
 #include <algorithm>
+#include <climits>
 
 namespace nc {
 namespace {
@@ -17,7 +18,6 @@ namespace {
 // A step with this many packed rows or fewer is planned by one block alone;
 // above it a second launch over many blocks writes the rows' positions and
 // slots.
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanFusedRows = 4096;
 // Blocks of a request checked by its own thread; longer runs take a warp.
 constexpr int kPlanOwn = 4;
@@ -37,47 +37,48 @@ struct PlanArgs {
     int* status;
 };
 
-// Exclusive prefix sums, in place, of three arrays of n ints in shared memory
-// (n <= kMaxRequests) by kPlanThreads threads; tot[i] gets the sums.
+// Exclusive prefix sums, in place, of three arrays of n <= NT * PER ints in shared
+// memory by the block's NT threads; tot[i] gets the sums.
+template <int NT, int PER>
 __device__ __forceinline__ void plan_scan3(int* a, int* b, int* c, int n, int* tot) {
-    constexpr int PER = kMaxRequests / kPlanThreads;
     __shared__ int ws[3][32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int lo = threadIdx.x * PER;
-    int va[PER], vb[PER], vc[PER], sa = 0, sb = 0, sc = 0;
+    const int lo = threadIdx.x * PER, used = (n + 32 * PER - 1) / (32 * PER);  // warps with a value
+    int va[PER], vb[PER], vc[PER], ia = 0, ib = 0, ic = 0;
+    if (w < used) {
+        int sa = 0, sb = 0, sc = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const bool in = lo + i < n;
-        va[i] = in ? a[lo + i] : 0; vb[i] = in ? b[lo + i] : 0; vc[i] = in ? c[lo + i] : 0;
-        sa += va[i]; sb += vb[i]; sc += vc[i];
-    }
-    int ia = sa, ib = sb, ic = sc;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ib, o),
-                  z = __shfl_up_sync(0xffffffffu, ic, o);
-        if (lane >= o) { ia += x; ib += y; ic += z; }
-    }
-    if (lane == 31) { ws[0][w] = ia; ws[1][w] = ib; ws[2][w] = ic; }
-    __syncthreads();
-    if (w < 3) {
-        int t = ws[w][lane];
+        for (int i = 0; i < PER; ++i) {
+            const bool in = lo + i < n;
+            va[i] = in ? a[lo + i] : 0; vb[i] = in ? b[lo + i] : 0; vc[i] = in ? c[lo + i] : 0;
+            sa += va[i]; sb += vb[i]; sc += vc[i];
+        }
+        ia = sa; ib = sb; ic = sc;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += x;
+            const int x = __shfl_up_sync(0xffffffffu, ia, o), y = __shfl_up_sync(0xffffffffu, ib, o),
+                      z = __shfl_up_sync(0xffffffffu, ic, o);
+            if (lane >= o) { ia += x; ib += y; ic += z; }
         }
-        ws[w][lane] = t;
+        if (lane == 31) { ws[0][w] = ia; ws[1][w] = ib; ws[2][w] = ic; }
+        ia -= sa; ib -= sb; ic -= sc;
     }
     __syncthreads();
-    ia += (w ? ws[0][w - 1] : 0) - sa; ib += (w ? ws[1][w - 1] : 0) - sb; ic += (w ? ws[2][w - 1] : 0) - sc;
+    int ta = 0, tb = 0, tc = 0;
+    for (int k = 0; k < used; ++k) {
+        const int xa = ws[0][k], xb = ws[1][k], xc = ws[2][k];
+        if (k < w) { ia += xa; ib += xb; ic += xc; }
+        ta += xa; tb += xb; tc += xc;
+    }
+    if (w < used) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (lo + i < n) {
-            a[lo + i] = ia; b[lo + i] = ib; c[lo + i] = ic;
-            ia += va[i]; ib += vb[i]; ic += vc[i];
-        }
-    tot[0] = ws[0][31]; tot[1] = ws[1][31]; tot[2] = ws[2][31];
+        for (int i = 0; i < PER; ++i)
+            if (lo + i < n) {
+                a[lo + i] = ia; b[lo + i] = ib; c[lo + i] = ic;
+                ia += va[i]; ib += vb[i]; ic += vc[i];
+            }
+    }
+    tot[0] = ta; tot[1] = tb; tot[2] = tc;
     __syncthreads();
 }
 
@@ -112,12 +113,14 @@ __device__ __forceinline__ void plan_row(const PlanArgs& p, const int* cu, const
 // timing.  Bound by latency, the chain lengths -> table -> stack -> table -> rows of
 // dependent global accesses, so every stage has all of its loads on their way at
 // once: a thread's requests with up to kPlanOwn blocks each, and for the others (long
-// chunks, released requests) a warp with kPlanWide blocks.
-constexpr int kPlanPer = kMaxRequests / kPlanThreads;  // requests of a thread
-constexpr int kPlanWide = 8 * 32;
-static_assert(kPlanOwn * kPlanPer <= 32, "a thread's blocks without a page are bits of a word");
+// chunks, released requests) a warp with kPlanWide blocks of kPlanKept requests, whose
+// table entries it keeps to the end.  512 requests, 48 with chunks and 32 released:
+// 16.4 us before that, FIGP after; four decoding requests: FIGQ.
+constexpr int kPlanWide = 8 * 32, kPlanKept = 3;
+constexpr int kPlanSmall = 128;  // requests that a block of as many threads plans
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs p, bool fill_rows) {
+template <int NT, int PER>
+__global__ void __launch_bounds__(NT) page_plan_kernel(const PlanArgs p, bool fill_rows) {
     extern __shared__ int sm[];
     __shared__ int s_bad, s_specials;
     __shared__ unsigned long long s_rows;
@@ -127,30 +130,27 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     int* s_back = s_need + p.n_req;      // pages it gives back, then their prefix
     int* s_cu = s_back + p.n_req;        // [n_req + 1]
     int* s_special = s_cu + p.n_req + 1; // requests that a warp looks after, 2 r + (released)
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = kPlanThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = NT / 32;
     const int shift = 31 - __clz(p.page);
     const long long cap = (long long)p.max_blocks << shift;
     auto held = [&](int e) { return (unsigned)e < (unsigned)p.n_pages; };
     auto row_of = [&](int r) { return p.table + (size_t)r * p.max_blocks; };
     auto first = [&](int r) { return s_cached[r] >> shift; };
     auto end = [&](int r) { return (int)(((long long)s_cached[r] + s_new[r] + p.page - 1) >> shift); };
-    // a warp's blocks lo .. hi - 1 of a row, kPlanWide at a time: f(entries, first block)
-    auto blocks = [&](const int32_t* row, int lo, int hi, auto f) {
-        for (int j0 = lo; j0 < hi; j0 += kPlanWide) {
-            int e[kPlanWide / 32];
+    struct Entries { int e[kPlanWide / 32]; };
+    auto entries = [&](const int32_t* row, int j0, int hi) {
+        Entries x;
 #pragma unroll
-            for (int u = 0; u < kPlanWide / 32; ++u) e[u] = j0 + 32 * u + lane < hi ? row[j0 + 32 * u + lane] : -1;
-            f(e, j0);
-        }
+        for (int u = 0; u < kPlanWide / 32; ++u) x.e[u] = j0 + 32 * u + lane < hi ? row[j0 + 32 * u + lane] : -1;
+        return x;
     };
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) { s_bad = 0; s_rows = 0; s_specials = 0; }
     const int count0 = *p.free_count;
     const int count = min(max(count0, 0), p.n_pages);
-    int cached[kPlanPer], fresh[kPlanPer], gone[kPlanPer];
+    int cached[PER], fresh[PER], gone[PER];
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-        const int r = tid + i * kPlanThreads;
+    for (int i = 0; i < PER; ++i) {
+        const int r = tid + i * NT;
         if (r >= p.n_req) break;
         cached[i] = p.cached[r];
         fresh[i] = p.new_len[r];
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     unsigned want = 0;  // bit kPlanOwn i + j: block j of the thread's i-th request needs a page
     unsigned long long rows = 0;
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
-        const int r = tid + i * kPlanThreads;
+    for (int i = 0; i < PER; ++i) {
+        const int r = tid + i * NT;
         if (r >= p.n_req) break;
         const bool rel = gone[i] != 0;
         const long long total = (long long)(rel ? 0 : cached[i]) + fresh[i];
@@ -188,23 +188,57 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     if (lane == 0 && rows) atomicAdd(&s_rows, rows);
     __syncthreads();
     const int specials = s_specials;  // in any order: what comes of them goes by the prefix sums
-    for (int i = warp; i < specials; i += nwarp) {
-        const int r = s_special[i] >> 1;
-        const bool rel = s_special[i] & 1;
-        int n = 0;
-        blocks(row_of(r), rel ? 0 : first(r), rel ? p.max_blocks : end(r), [&](const int* e, int j0) {
+    // the warp's i-th: request, released or not, and its blocks lo .. hi - 1 that matter
+    struct Special { int r, lo, hi; bool rel; };
+    auto special = [&](int i) {
+        Special s;
+        s.r = s_special[i] >> 1;
+        s.rel = s_special[i] & 1;
+        s.lo = s.rel ? 0 : first(s.r);
+        s.hi = s.rel ? p.max_blocks : end(s.r);
+        return s;
+    };
+    Entries kept[kPlanKept];
 #pragma unroll
-            for (int u = 0; u < kPlanWide / 32; ++u) n += rel ? held(e[u]) : j0 + 32 * u + lane < end(r) && !held(e[u]);
-        });
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) {
-            s_need[r] = rel ? end(r) : n;
-            s_back[r] = rel ? n : 0;
+    for (int k = 0; k < kPlanKept; ++k)
+        if (warp + k * nwarp < specials) {
+            const Special s = special(warp + k * nwarp);
+            kept[k] = entries(row_of(s.r), s.lo, s.hi);
         }
-    }
+    // f(special, entries, first block) over all blocks of the warp's specials, the kept entries first
+    auto each = [&](auto begin, auto f, auto done) {
+#pragma unroll
+        for (int k = 0; k < kPlanKept; ++k)
+            if (warp + k * nwarp < specials) {
+                const Special s = special(warp + k * nwarp);
+                begin(s);
+                f(s, kept[k], s.lo);
+                for (int j = s.lo + kPlanWide; j < s.hi; j += kPlanWide) f(s, entries(row_of(s.r), j, s.hi), j);
+                done(s);
+            }
+        for (int i = warp + kPlanKept * nwarp; i < specials; i += nwarp) {
+            const Special s = special(i);
+            begin(s);
+            for (int j = s.lo; j < s.hi; j += kPlanWide) f(s, entries(row_of(s.r), j, s.hi), j);
+            done(s);
+        }
+    };
+    int n = 0;
+    each([&](const Special&) { n = 0; },
+         [&](const Special& s, const Entries& x, int j0) {
+#pragma unroll
+             for (int u = 0; u < kPlanWide / 32; ++u) n += s.rel ? held(x.e[u]) : j0 + 32 * u + lane < s.hi && !held(x.e[u]);
+         },
+         [&](const Special& s) {
+             n = __reduce_add_sync(0xffffffffu, n);
+             if (lane == 0) {
+                 s_need[s.r] = s.rel ? end(s.r) : n;
+                 s_back[s.r] = s.rel ? n : 0;
+             }
+         });
     __syncthreads();
     int tot[3];
-    plan_scan3(s_need, s_back, s_cu, p.n_req, tot);
+    plan_scan3<NT, PER>(s_need, s_back, s_cu, p.n_req, tot);
     const int need_all = tot[0], back_all = tot[1];
     const int grown = min(count + back_all, p.n_pages);
     int refused = s_bad;
@@ -212,12 +246,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     if (!refused && need_all > grown) refused |= ST_OUT_OF_PAGES;
     if (refused) {  // nothing changes, and the step has no rows
         if (tid == 0) set_status(p.status, refused);
-        for (int r = tid; r <= p.n_req; r += kPlanThreads) {
+        for (int r = tid; r <= p.n_req; r += NT) {
             p.cu_rows[r] = 0;
             if (r < p.n_req) p.kv_len[r] = p.cached[r];
         }
         if (fill_rows)
-            for (int i = tid; i < p.rows; i += kPlanThreads) { p.positions[i] = 0; p.slots[i] = -1; }
+            for (int i = tid; i < p.rows; i += NT) { p.positions[i] = 0; p.slots[i] = -1; }
         return;
     }
     if (tid == 0) {
@@ -225,30 +259,30 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
         *p.free_count = grown - need_all;
         if (count != count0 || count + back_all > p.n_pages) set_status(p.status, ST_BAD_PAGE);
     }
-    if (back_all)
-        for (int i = warp; i < specials; i += nwarp) {
-            if (!(s_special[i] & 1)) continue;
-            const int r = s_special[i] >> 1;
-            int at = count + s_back[r];
-            blocks(row_of(r), 0, p.max_blocks, [&](const int* e, int j0) {
+    if (back_all) {
+        int at = 0;
+        each([&](const Special& s) { at = count + s_back[s.r]; },
+             [&](const Special& s, const Entries& x, int j0) {
+                 if (!s.rel) return;
 #pragma unroll
-                for (int u = 0; u < kPlanWide / 32; ++u) {
-                    const unsigned m = __ballot_sync(0xffffffffu, held(e[u]));
-                    if (held(e[u])) {
-                        const int to = at + __popc(m & ((1u << lane) - 1));
-                        if (to < p.n_pages) p.free_pages[to] = e[u];
-                        row_of(r)[j0 + 32 * u + lane] = -1;
-                    }
-                    at += __popc(m);
-                }
-            });
-        }
+                 for (int u = 0; u < kPlanWide / 32; ++u) {
+                     const unsigned m = __ballot_sync(0xffffffffu, held(x.e[u]));
+                     if (held(x.e[u])) {
+                         const int to = at + __popc(m & ((1u << lane) - 1));
+                         if (to < p.n_pages) p.free_pages[to] = x.e[u];
+                         row_of(s.r)[j0 + 32 * u + lane] = -1;
+                     }
+                     at += __popc(m);
+                 }
+             },
+             [&](const Special&) {});
+    }
     __syncthreads();
     if (need_all) {
-        int page[kPlanPer * kPlanOwn];
+        int page[PER * kPlanOwn];
 #pragma unroll
-        for (int i = 0; i < kPlanPer; ++i) {
-            const int r = tid + i * kPlanThreads;
+        for (int i = 0; i < PER; ++i) {
+            const int r = tid + i * NT;
             if (r >= p.n_req) break;
             int from = grown - 1 - s_need[r];
 #pragma unroll
@@ -256,39 +290,69 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
                 if (want >> (kPlanOwn * i + j) & 1) page[kPlanOwn * i + j] = p.free_pages[from--];
         }
 #pragma unroll
-        for (int i = 0; i < kPlanPer; ++i) {
-            const int r = tid + i * kPlanThreads;
+        for (int i = 0; i < PER; ++i) {
+            const int r = tid + i * NT;
             if (r >= p.n_req) break;
 #pragma unroll
             for (int j = 0; j < kPlanOwn; ++j)
                 if (want >> (kPlanOwn * i + j) & 1) row_of(r)[first(r) + j] = page[kPlanOwn * i + j];
         }
-        for (int i = warp; i < specials; i += nwarp) {
-            const int r = s_special[i] >> 1;
-            const bool rel = s_special[i] & 1;  // its row is empty by now
-            int from = grown - 1 - s_need[r];
-            blocks(row_of(r), first(r), end(r), [&](const int* e, int j0) {
-                int got[kPlanWide / 32];
+        // every page's place first, all of the warp's loads on their way, then the table
+        Entries got[kPlanKept];
+        int from = 0;
+        auto take = [&](const Special& s, const Entries& x, int j0, Entries& y) {
 #pragma unroll
-                for (int u = 0; u < kPlanWide / 32; ++u) {
-                    const bool need = j0 + 32 * u + lane < end(r) && (rel || !held(e[u]));
-                    const unsigned m = __ballot_sync(0xffffffffu, need);
-                    got[u] = need ? p.free_pages[from - __popc(m & ((1u << lane) - 1))] : -1;
-                    from -= __popc(m);
+            for (int u = 0; u < kPlanWide / 32; ++u) {
+                const int j = j0 + 32 * u + lane;
+                const bool need = j < end(s.r) && (s.rel || !held(x.e[u]));  // a released row is empty by now
+                const unsigned m = __ballot_sync(0xffffffffu, need);
+                y.e[u] = need ? p.free_pages[from - __popc(m & ((1u << lane) - 1))] : INT_MIN;
+                from -= __popc(m);
+            }
+        };
+        auto put = [&](const Special& s, int j0, const Entries& y) {
+#pragma unroll
+            for (int u = 0; u < kPlanWide / 32; ++u)
+                if (y.e[u] != INT_MIN) row_of(s.r)[j0 + 32 * u + lane] = y.e[u];
+        };
+        int next[kPlanKept];
+#pragma unroll
+        for (int k = 0; k < kPlanKept; ++k)
+            if (warp + k * nwarp < specials) {
+                const Special s = special(warp + k * nwarp);
+                from = grown - 1 - s_need[s.r];
+                take(s, kept[k], s.lo, got[k]);
+                next[k] = from;
+            }
+#pragma unroll
+        for (int k = 0; k < kPlanKept; ++k)
+            if (warp + k * nwarp < specials) {
+                const Special s = special(warp + k * nwarp);
+                put(s, s.lo, got[k]);
+                from = next[k];
+                for (int j = s.lo + kPlanWide; j < end(s.r); j += kPlanWide) {
+                    Entries y;
+                    take(s, entries(row_of(s.r), j, s.hi), j, y);
+                    put(s, j, y);
                 }
-#pragma unroll
-                for (int u = 0; u < kPlanWide / 32; ++u)
-                    if (j0 + 32 * u + lane < end(r) && (rel || !held(e[u]))) row_of(r)[j0 + 32 * u + lane] = got[u];
-            });
+            }
+        for (int i = warp + kPlanKept * nwarp; i < specials; i += nwarp) {
+            const Special s = special(i);
+            from = grown - 1 - s_need[s.r];
+            for (int j = s.lo; j < end(s.r); j += kPlanWide) {
+                Entries y;
+                take(s, entries(row_of(s.r), j, s.hi), j, y);
+                put(s, j, y);
+            }
         }
     }
-    for (int r = tid; r <= p.n_req; r += kPlanThreads) {
+    for (int r = tid; r <= p.n_req; r += NT) {
         p.cu_rows[r] = s_cu[r];
         if (r < p.n_req) p.kv_len[r] = s_cached[r] + s_new[r];
     }
     __syncthreads();
     if (fill_rows)
-        for (int i = tid; i < p.rows; i += kPlanThreads) plan_row(p, s_cu, s_cached, shift, i);
+        for (int i = tid; i < p.rows; i += NT) plan_row(p, s_cu, s_cached, shift, i);
 }
 
 // Positions and slots of the rows, over many blocks.
@@ -565,10 +629,14 @@ cudaError_t launch_page_plan(int n_req, int page, int max_blocks, int n_pages, i
                              int32_t* slots, int* status, cudaStream_t s) {
     const PlanArgs p{n_req, page, max_blocks, n_pages, rows, cached, new_len, release, table, free_pages, free_count,
                      cu_rows, kv_len, positions, slots, status};
-    cudaError_t e = ensure_smem_limit((const void*)page_plan_kernel, (6 * kMaxRequests + 1) * 4);
+    constexpr int kLarge = 1024;
+    auto large = page_plan_kernel<kLarge, kMaxRequests / kLarge>;
+    cudaError_t e = ensure_smem_limit((const void*)large, (6 * kMaxRequests + 1) * 4);
     if (e != cudaSuccess) return e;
     const bool fused = rows <= kPlanFusedRows;
-    page_plan_kernel<<<1, kPlanThreads, (6 * n_req + 1) * 4, s>>>(p, fused);
+    // few requests and rows: a small block starts and meets sooner
+    if (n_req <= kPlanSmall && rows <= 4 * kPlanSmall) page_plan_kernel<kPlanSmall, 1><<<1, kPlanSmall, (6 * n_req + 1) * 4, s>>>(p, fused);
+    else large<<<1, kLarge, (6 * n_req + 1) * 4, s>>>(p, fused);
     count_launch();
     if (!fused) {
         const int blocks = std::min((rows + 255) / 256, 4 * device_sm_count());
