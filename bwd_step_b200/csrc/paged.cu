@@ -110,12 +110,13 @@ __device__ __forceinline__ void plan_row(const PlanArgs& p, const int* cu, const
 // One block.  Per request, the blocks that need a page and the pages that it gives
 // back; their prefix sums; then pages go back onto the stack and are taken from its
 // top, each at the place that its prefix names, so that the result does not depend on
-// timing.  Bound by latency, the chain lengths -> table -> stack -> table -> rows of
-// dependent global accesses, so every stage has all of its loads on their way at
-// once: a thread's requests with up to kPlanOwn blocks each, and for the others (long
-// chunks, released requests) a warp with kPlanWide blocks of kPlanKept requests, whose
-// table entries it keeps to the end.  512 requests, 48 with chunks and 32 released:
-// 16.4 us before that, FIGP after; four decoding requests: FIGQ.
+// timing.  Bound by latency: the chain lengths -> table -> stack -> table -> rows of
+// dependent global accesses, and the first run of every stage's code.  So every stage
+// has its loads on their way together: a thread's requests with up to kPlanOwn blocks
+// each, and for the others (long chunks, released requests) a warp with kPlanWide
+// blocks of kPlanKept requests, whose table entries it keeps to the end.  512 requests,
+// 48 of them with chunks and 32 released: 16.4 us (34.6 with one window at a time);
+// four decoding requests: 2.9 us in a graph (3.7 with 1024 threads).
 constexpr int kPlanWide = 8 * 32, kPlanKept = 3;
 constexpr int kPlanSmall = 128;  // requests that a block of as many threads plans
 
