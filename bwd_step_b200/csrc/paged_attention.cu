@@ -26,8 +26,8 @@ using namespace tc;
 
 constexpr int kTile = 64;        // keys of a decode tile
 // Where the table has no more positions than this, nothing is cut over blocks and there is nothing to
-// join.  Steps with chunks: 8 prompts of some 225 rows on up to 700 positions took 30.1 us instead of
-// 34.8 (26.9 by now).  Steps of decoding requests alone, whose join is most of what they do: four requests of up to
+// join.  Steps with chunks: 8 prompts of some 225 rows on up to 700 positions save 4.7 us of the 31.6
+// that they take when cut.  Steps of decoding requests alone, whose join is most of what they do: four requests of up to
 // 700 positions take 12.4 us whole and 10.3 cut, so only tables of a few tiles.
 constexpr int kWholePositions = 1024, kWholeDecoding = 256;
 constexpr int kDecRows = 16;     // query heads of a K/V head that the decode kernel takes
