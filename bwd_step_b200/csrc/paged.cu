@@ -597,12 +597,99 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const ReorderArgs a) 
     }
 }
 
+// More beams than a thread holds: 2 or 4 groups of threads share an element's changing
+// beams, U each.  They load the parents' vectors, all on their way at once, meet, and
+// store them.  Against one thread for up to 32 beams: 5 x 12 beams, 18 layers, 3
+// positions of 128 in pages 39 -> 16 us; 10 x 9 beams, 6 layers, up to 118 positions of
+// 512 bytes in pages 54 -> 28; 9 x 9 beams, 18 layers of 175 positions of 320, dense
+// (472 MB) 121 -> 118.
+template <int U, bool PAGED>
+__global__ void __launch_bounds__(256) beam_reorder_many_kernel(const ReorderArgs a) {
+    __shared__ int s_from[32], s_to[32], s_lo[32], s_hi[32];  // the changing beams: rows, positions
+    __shared__ int s_n, s_first, s_last;
+    const unsigned vecs = (unsigned)a.width >> 4;
+    const int tid = threadIdx.x, shift = PAGED ? 31 - __clz(a.page) : 0;
+    const int cap = PAGED ? (int)min((long long)a.max_blocks * a.page, 0x7fffffffll) : a.t_max;
+    for (int pb = blockIdx.y; pb < a.planes * a.batch; pb += gridDim.y) {
+        const int plane = pb / a.batch, b = pb % a.batch;
+        __syncthreads();
+        if (tid < 32) {
+            const int row = b * a.beams + tid;
+            int par = tid, lo = 0, hi = 0;
+            if (tid < a.beams) {
+                par = a.parents[row];
+                lo = PAGED ? max(a.starts[row], 0) : a.start;
+                hi = PAGED ? min(a.ends[row], cap) : a.end;
+                if ((unsigned)par >= (unsigned)a.beams) {
+                    set_status(a.status, ST_BAD_LENGTH);
+                    par = tid;
+                }
+            }
+            const bool moves = par != tid && lo < hi;
+            const unsigned m = __ballot_sync(0xffffffffu, moves);
+            if (moves) {
+                const int k = __popc(m & ((1u << tid) - 1));
+                s_from[k] = b * a.beams + par;
+                s_to[k] = row;
+                s_lo[k] = lo;
+                s_hi[k] = hi;
+            }
+            const int first = __reduce_min_sync(0xffffffffu, moves ? lo : 0x7fffffff), last = __reduce_max_sync(0xffffffffu, moves ? hi : 0);
+            if (tid == 0) { s_n = __popc(m); s_first = first; s_last = last; }
+        }
+        __syncthreads();
+        const int n = s_n;
+        if (n == 0) continue;
+        const int lo = s_first, groups = n <= U ? 1 : n <= 2 * U ? 2 : 4, E = 256 / groups;
+        const int x = tid & (E - 1), k0 = tid / E * U;  // element of the block's, first of the thread's beams
+        const long long total = (long long)(s_last - lo) * vecs;
+        char* base = a.base + (size_t)plane * a.plane_stride;
+        for (long long at = (long long)blockIdx.x * E; at < total; at += (long long)gridDim.x * E) {
+            const long long xx = at + x;
+            // (32-bit division where the span allows it)
+            const unsigned rel = total <= 0xffffffffll ? (unsigned)xx / vecs : (unsigned)(xx / vecs);
+            const int pos = lo + (int)rel;
+            const size_t e = (size_t)(xx - (long long)rel * vecs) << 4;
+            uint4 v[U];
+            char* to[U];
+            auto addr = [&](int row) -> char* {  // null: the position has no page
+                if (!PAGED) return base + ((size_t)row * a.t_max + pos) * a.width + e;
+                const int page = a.table[(size_t)row * a.max_blocks + (pos >> shift)];
+                if ((unsigned)page >= (unsigned)a.n_pages) return nullptr;
+                return base + (((size_t)page << shift) + (pos & (a.page - 1))) * a.width + e;
+            };
+            const char* from[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u;
+                const bool in = xx < total && k < n && pos >= s_lo[k] && pos < s_hi[k];
+                from[u] = to[u] = nullptr;
+                if (in) {
+                    from[u] = addr(s_from[k]);
+                    to[u] = addr(s_to[k]);
+                    if (PAGED && (!from[u] || !to[u])) {
+                        set_status(a.status, ST_BAD_PAGE);
+                        to[u] = nullptr;
+                    }
+                    if (from[u] == to[u]) to[u] = nullptr;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (to[u]) v[u] = *reinterpret_cast<const uint4*>(from[u]);
+            if (groups > 1) __syncthreads();  // else a thread has all of an element's beams
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (to[u]) *reinterpret_cast<uint4*>(to[u]) = v[u];
+        }
+    }
+}
+
 template <bool PAGED>
 void reorder_launch(const ReorderArgs& a, dim3 grid, cudaStream_t s) {
     if (a.beams <= 4) beam_reorder_kernel<4, PAGED><<<grid, 256, 0, s>>>(a);
     else if (a.beams <= 8) beam_reorder_kernel<8, PAGED><<<grid, 256, 0, s>>>(a);
-    else if (a.beams <= 16) beam_reorder_kernel<16, PAGED><<<grid, 256, 0, s>>>(a);
-    else beam_reorder_kernel<32, PAGED><<<grid, 256, 0, s>>>(a);
+    else beam_reorder_many_kernel<8, PAGED><<<grid, 256, 0, s>>>(a);
 }
 
 template <typename A>
@@ -698,7 +785,7 @@ cudaError_t launch_beam_reorder(const ReorderArgs& a, cudaStream_t s) {
     const long long n = span * (a.width / 16);
     if (n <= 0) return cudaSuccess;
     const unsigned gy = (unsigned)std::min(65535ll, (long long)a.planes * a.batch);
-    const long long want = std::max(1ll, 16ll * device_sm_count() / gy);  // blocks along a span, enough to fill the GPU
+    const long long want = std::max(1ll, (a.table && a.beams > 8 ? 8ll : 16ll) * device_sm_count() / gy);  // blocks along a span, enough to fill the GPU
     const dim3 grid((unsigned)std::min((n + 255) / 256, want), gy);
     if (a.table) reorder_launch<true>(a, grid, s);
     else reorder_launch<false>(a, grid, s);
