@@ -92,7 +92,8 @@ def _run_plan(m, page, cached, new, release, table, free, count, rows, kv_alias=
 
 @pytest.mark.parametrize("n_req,page,max_blocks,chunk,pad", [
     (1, 16, 1, 1, 0), (1, 256, 3, 300, 1), (3, 16, 9, 40, 5), (31, 32, 40, 200, 0), (33, 64, 12, 65, 7),
-    (200, 16, 70, 1, 0), (300, 16, 33, 100, 11), (1500, 128, 5, 30, 3), (4096, 16, 4, 2, 0)])
+    (200, 16, 70, 1, 0), (300, 16, 33, 100, 11), (1500, 128, 5, 30, 3), (4096, 16, 4, 2, 0),
+    (5, 16, 700, 6000, 3), (150, 16, 530, 5000, 0), (128, 32, 9, 3, 1)])
 @pytest.mark.parametrize("rel_share", [0.0, 0.3, 1.0])
 def test_plan_matches_a_plain_allocator(n_req, page, max_blocks, chunk, pad, rel_share):
     rng = random.Random(n_req * 7 + page)
@@ -137,6 +138,15 @@ def test_a_refused_step_changes_nothing(what):
     assert got == [before, free, count, [0] * 21, cached, [0] * rows, [-1] * rows]
     assert m.check() == (_lib.NC_ERR_OUT_OF_PAGES if what == "pages" else _lib.NC_ERR_BAD_LENGTH)
     assert m.check() == 0
+
+
+def test_a_free_page_outside_the_cache_is_reported():
+    """What the stack holds goes to the table, but to no slot."""
+    m = _model()
+    _, got = _run_plan(m, 16, [0, 0], [3, 20], None, [[-1, -1], [-1, -1]], [1 << 28, 2, -5, 1], 4, 23)
+    assert m.check() == _lib.NC_ERR_BAD_PAGE
+    assert got[0][0][0] == 1 and got[6][:3] == [16, 17, 18]
+    assert got[6][3:] == [-1] * 16 + [32, 33, 34, 35]
 
 
 # ---------------------------------------------------------------- attention
@@ -262,7 +272,7 @@ def test_attention_fp32(h, nkv, hd, lens, page):
 
 @pytest.mark.parametrize("lens", [[(0, 1)], [(4000, 1)], [(9000, 3)], [(2000, 40)], [(0, 700)], [(5000, 300), (10, 1)],
                                   [(0, 0), (0, 1)], [(700, 1)] * 150, [(60, 2)] * 97, [(260, 30)] * 40,
-                                  [(3000, 9)] * 20 + [(1, 1)] * 3, [(0, 0)] * 5 + [(77, 5)] + [(0, 0)] * 4])
+                                  [(30, 1), (200, 1), (64, 1), (1, 1)] * 60, [(3000, 9)] * 20 + [(1, 1)] * 3, [(0, 0)] * 5 + [(77, 5)] + [(0, 0)] * 4])
 @pytest.mark.parametrize("h,hd", [(10, 128), (12, 64)])
 def test_attention_batches(lens, h, hd):
     """Few long requests, many short ones, and both kinds of step at once."""
