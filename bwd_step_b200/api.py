@@ -125,6 +125,7 @@ class Model:
         _ok(lib().nc_model_create(ctypes.byref(self.cfg), PRECISIONS[precision], ctypes.byref(h)),
             "nc_model_create")
         self._h = h
+        self._handle, self._bf16 = h.value, precision == "bf16"  # what the serving calls need
         import torch
         # nc_model_create bound the model to the current device; every device
         # tensor handed to it later must live there
@@ -133,21 +134,13 @@ class Model:
     def close(self):
         if getattr(self, "_h", None):
             lib().nc_model_destroy(self._h)
-            self._h = None
+            self._h = self._handle = None
 
     def __del__(self):
         try:
             self.close()
         except Exception:
             pass
-
-    @property
-    def _handle(self):
-        return self._h.value if self._h else None
-
-    @property
-    def _bf16(self):
-        return self.precision == "bf16"
 
     @property
     def weight_dtype(self):
@@ -272,9 +265,10 @@ class Model:
         pages given back (release [R]) and taken (block_table [R, blocks],
         free_pages [pages], free_count [1], in place), row offsets cu_rows [R + 1],
         lengths kv_len [R], and positions and slots [rows] of the packed rows."""
-        code = _serving().page_plan(self._handle, self.device, page_size, cached_len, new_len, release, block_table,
-                                    free_pages, free_count, cu_rows, kv_len, positions, slots,
-                                    _stream_of(stream, self.device))
+        serving = _serving_module or _serving()
+        code = serving.page_plan(self._handle, self.device, page_size, cached_len, new_len, release, block_table,
+                                 free_pages, free_count, cu_rows, kv_len, positions, slots,
+                                 _stream_of(stream, self.device))
         if code:
             _ok(code, "nc_page_plan")
 
@@ -285,9 +279,10 @@ class Model:
         n_head head_dim] of the rows qkv [rows, (n_head + 2 n_kv_head) head_dim]
         over their requests' positions.  max_new bounds a request's new rows."""
         c = self.cfg
-        code = _serving().paged_attention(self._handle, self.device, self._bf16, c.n_head, c.n_kv_head, c.head_dim, max_new,
-                                          cu_rows, kv_len, slots, block_table, qkv, k_pages, v_pages, o, workspace,
-                                          _stream_of(stream, self.device))
+        serving = _serving_module or _serving()
+        code = serving.paged_attention(self._handle, self.device, self._bf16, c.n_head, c.n_kv_head, c.head_dim, max_new,
+                                       cu_rows, kv_len, slots, block_table, qkv, k_pages, v_pages, o, workspace,
+                                       _stream_of(stream, self.device))
         if code:
             _ok(code, "nc_paged_attention")
 
@@ -297,9 +292,10 @@ class Model:
         pages, page_size, n_kv_head, head_dim]: packed tokens [rows], the logits of
         every request's last new token into logits [requests, V]."""
         c = self.cfg
-        code = _serving().paged_forward(self._handle, self.device, self._bf16, c.n_layer, c.n_kv_head, c.head_dim, c.vocab,
-                                        self.num_params(), max_new, cu_rows, kv_len, slots, block_table, tokens, positions,
-                                        weights, kv_pages, logits, workspace, _stream_of(stream, self.device))
+        serving = _serving_module or _serving()
+        code = serving.paged_forward(self._handle, self.device, self._bf16, c.n_layer, c.n_kv_head, c.head_dim, c.vocab,
+                                     self.num_params(), max_new, cu_rows, kv_len, slots, block_table, tokens, positions,
+                                     weights, kv_pages, logits, workspace, _stream_of(stream, self.device))
         if code:
             _ok(code, "nc_paged_forward")
 
@@ -309,8 +305,9 @@ class Model:
         V]) and scores [batch, beams] the best candidates of every batch row into
         scores_out, tokens and parents [batch, beams], and finished_out where beams
         end at eos (finished, finished_out int32 [batch, beams])."""
-        code = _serving().beam_select(self._handle, self.device, self._bf16, self.cfg.vocab, eos, logits, scores, finished,
-                                      scores_out, tokens, parents, finished_out, _stream_of(stream, self.device))
+        serving = _serving_module or _serving()
+        code = serving.beam_select(self._handle, self.device, self._bf16, self.cfg.vocab, eos, logits, scores, finished,
+                                   scores_out, tokens, parents, finished_out, _stream_of(stream, self.device))
         if code:
             _ok(code, "nc_beam_select")
 
@@ -319,8 +316,9 @@ class Model:
         back-pointers parents [batch, beams] (int32), in place."""
         c = self.cfg
         each = c.n_layer * 2 * c.n_kv_head * c.head_dim * (2 if self._bf16 else 4)
-        code = _serving().beam_reorder(self._handle, self.device, each, kv_cache, T_max, parents, start, end,
-                                       _stream_of(stream, self.device))
+        serving = _serving_module or _serving()
+        code = serving.beam_reorder(self._handle, self.device, each, kv_cache, T_max, parents, start, end,
+                                    _stream_of(stream, self.device))
         if code:
             _ok(code, "nc_beam_reorder")
 
@@ -329,9 +327,10 @@ class Model:
         back-pointers parents [batch, beams], in place; block_table [batch * beams,
         blocks], starts and ends [batch * beams] (all int32)."""
         c = self.cfg
-        code = _serving().beam_reorder_paged(self._handle, self.device, self._bf16, c.n_layer, c.n_kv_head, c.head_dim,
-                                             kv_pages, parents, block_table, starts, ends,
-                                             _stream_of(stream, self.device))
+        serving = _serving_module or _serving()
+        code = serving.beam_reorder_paged(self._handle, self.device, self._bf16, c.n_layer, c.n_kv_head, c.head_dim,
+                                          kv_pages, parents, block_table, starts, ends,
+                                          _stream_of(stream, self.device))
         if code:
             _ok(code, "nc_beam_reorder_paged")
 

@@ -15,6 +15,7 @@ def _model():
     """A model without a handle: the library refuses it, the binding checks as ever."""
     m = object.__new__(Model)
     m._h, m.device, m.precision = None, 0, "bf16"
+    m._handle, m._bf16 = None, True
     m.cfg = types.SimpleNamespace(n_layer=2, n_head=4, n_kv_head=1, head_dim=64, vocab=512)
     return m
 
