@@ -368,11 +368,12 @@ __global__ void __launch_bounds__(256) page_rows_kernel(const PlanArgs p) {
 }
 
 // ---------------------------------------------------------------- cache writes
-template <typename A>
-__global__ void __launch_bounds__(256) paged_append_kernel(const A* __restrict__ qkv, int H, int nkv, int hd, int rows,
-                                                           const int32_t* __restrict__ slots, A* __restrict__ kc,
-                                                           A* __restrict__ vc, int n_slots, int* status) {
-    constexpr int VEC = Vec<A>::N;
+// (For the tensor-core attention of more than 16 query heads to a K/V head; the other kernels write
+// the cache themselves.)
+__global__ void __launch_bounds__(256) paged_append_kernel(const bf16* __restrict__ qkv, int H, int nkv, int hd, int rows,
+                                                           const int32_t* __restrict__ slots, bf16* __restrict__ kc,
+                                                           bf16* __restrict__ vc, int n_slots, int* status) {
+    constexpr int VEC = Vec<bf16>::N;
     const int kvn = nkv * hd, per_row = 2 * kvn / VEC;  // vectors of k then v
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= (long long)rows * per_row) return;
@@ -382,8 +383,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const A* __restrict__
         if (slot >= 0) set_status(status, ST_BAD_PAGE);
         return;
     }
-    const A* src = qkv + (size_t)r * ((H + 2 * nkv) * hd) + (size_t)H * hd + e;
-    A* dst = (e < kvn ? kc : vc) + (size_t)slot * kvn + (e < kvn ? e : e - kvn);
+    const bf16* src = qkv + (size_t)r * ((H + 2 * nkv) * hd) + (size_t)H * hd + e;
+    bf16* dst = (e < kvn ? kc : vc) + (size_t)slot * kvn + (e < kvn ? e : e - kvn);
     *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
 }
 
@@ -745,19 +746,11 @@ cudaError_t launch_page_plan(int n_req, int page, int max_blocks, int n_pages, i
     return cudaGetLastError();
 }
 
-cudaError_t launch_paged_append(DType at, const void* qkv, int H, int nkv, int hd, int rows, const int32_t* slots,
-                                const PagedKv& kv, int* status, cudaStream_t s) {
-    const long long n = (long long)rows * (2ll * nkv * hd * (long long)dt_size(at) / 16);
-    const unsigned blocks = (unsigned)((n + 255) / 256);
-    const int n_slots = kv.n_pages * kv.page;
-    if (at == DT_BF16)
-        paged_append_kernel<bf16><<<blocks, 256, 0, s>>>(reinterpret_cast<const bf16*>(qkv), H, nkv, hd, rows, slots,
-                                                         reinterpret_cast<bf16*>(kv.k), reinterpret_cast<bf16*>(kv.v),
-                                                         n_slots, status);
-    else
-        paged_append_kernel<float><<<blocks, 256, 0, s>>>(reinterpret_cast<const float*>(qkv), H, nkv, hd, rows, slots,
-                                                          reinterpret_cast<float*>(kv.k),
-                                                          reinterpret_cast<float*>(kv.v), n_slots, status);
+cudaError_t launch_paged_append(const bf16* qkv, int H, int nkv, int hd, int rows, const int32_t* slots, const PagedKv& kv,
+                                int* status, cudaStream_t s) {
+    const long long n = (long long)rows * (2ll * nkv * hd / Vec<bf16>::N);
+    paged_append_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(qkv, H, nkv, hd, rows, slots, reinterpret_cast<bf16*>(kv.k),
+                                                                    reinterpret_cast<bf16*>(kv.v), kv.n_pages * kv.page, status);
     count_launch();
     return cudaGetLastError();
 }

@@ -3,6 +3,8 @@
 #pragma once
 #include "kernels.h"
 
+#include <cuda_bf16.h>
+
 struct nc_model;
 
 namespace nc {
@@ -32,7 +34,7 @@ cudaError_t launch_page_plan(int n_req, int page, int max_blocks, int n_pages, i
                              int32_t* slots, int* status, cudaStream_t s);
 
 // The k, v heads of the packed qkv rows to their cache slots (slot < 0: the row has none).
-cudaError_t launch_paged_append(DType at, const void* qkv, int H, int nkv, int hd, int rows, const int32_t* slots,
+cudaError_t launch_paged_append(const __nv_bfloat16* qkv, int H, int nkv, int hd, int rows, const int32_t* slots,
                                 const PagedKv& kv, int* status, cudaStream_t s);
 
 // The rows' k, v to their slots and o[row, h] = softmax over the keys at positions 0..pos(row) of the

@@ -1286,7 +1286,7 @@ cudaError_t attention(const bf16* qkv, int H, int nkv, int rows, int max_new, co
         count_launch();
         e = cudaGetLastError();
     } else {
-        e = launch_paged_append(DT_BF16, qkv, H, nkv, HD, rows, slots, kv, status, s);
+        e = launch_paged_append(qkv, H, nkv, HD, rows, slots, kv, status, s);
     }
     if (e != cudaSuccess) return e;
     if (chunks) {
