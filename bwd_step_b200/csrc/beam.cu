@@ -16,6 +16,10 @@
 //   3. only the threads whose maximum reaches that bound, some K of all, read their
 //      values again (from L2) and hand the first block the candidates that reach it;
 //   4. the first block ranks those by counting the better ones.
+// The sums are kept in 32 bits.  A term e^d is off by 2.3 |d| 2^-24 of itself (the difference, the factor and
+// the product rounded; the mean of |d| over the terms by their weight is at most ln V) and by 2^-22
+// (ex2.approx), each change of the maximum on its way by 5 2^-24, each sum by 2^-24: some 60 2^-24 in
+// all for 65536 ids, so the log-sum-exp is within 2^-18 whatever the size of the logits.
 // One launch, no workspace.  64 x 8 beams of 65536 ids (62 MB) take 27 us: the stream
 // 11.5, bound by HBM, and what follows it by the latency of its steps; 1 x 4 beams 11.5 us.
 #include "paged.h"
@@ -197,8 +201,9 @@ __global__ void __launch_bounds__(kThreads + 32, 4) beam_select_kernel(const A* 
                     top = up;
                 }
                 if (top == -INFINITY) continue;
-                const float shift = -top * kLog2e;
-                const uint64_t l2 = tc::f2_pack(kLog2e, kLog2e), sh2 = tc::f2_pack(shift, shift);
+                // The difference before the factor: it is exact near the maximum, where -top * log2 e, rounded beside
+                // fma(z, log2 e, .), would leave |top| 2^-24 in the sum (and infinities at the type's largest values).
+                const uint64_t l2 = tc::f2_pack(kLog2e, kLog2e), less = tc::f2_pack(-top, -top);
                 uint64_t s2[2] = {tc::f2_pack(0.f, 0.f), tc::f2_pack(0.f, 0.f)};
 #pragma unroll
                 for (int q = 0; q < NV; ++q) {
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(kThreads + 32, 4) beam_select_kernel(const A* 
 #pragma unroll
                         for (int e = 0; e < VEC; e += 2) {
                             float x0, x1;
-                            tc::f2_unpack(tc::f2_fma(tc::f2_pack(v[e], v[e + 1]), l2, sh2), x0, x1);
+                            tc::f2_unpack(tc::f2_mul(tc::f2_add(tc::f2_pack(v[e], v[e + 1]), less), l2), x0, x1);
                             s2[(e >> 1) & 1] = tc::f2_add(s2[(e >> 1) & 1], tc::f2_pack(tc::ex2(x0), tc::ex2(x1)));
                         }
                 }
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(kThreads + 32, 4) beam_select_kernel(const A* 
                         load_vec(reinterpret_cast<const A*>(&raw[q]), v);
                         if ((q * kThreads + tid) * VEC < n)
 #pragma unroll
-                            for (int e = 0; e < VEC; ++e) add += tc::ex2(fmaf(fmaxf(v[e], -INFINITY), kLog2e, shift));
+                            for (int e = 0; e < VEC; ++e) add += tc::ex2((fmaxf(v[e], -INFINITY) - top) * kLog2e);
                     }
                 }
                 sum += add;

@@ -312,12 +312,17 @@ int nc_paged_forward(nc_model* m, const int32_t* tokens, int rows, int n_req, in
  *   scores[k] + logits[k][v] - logsumexp(logits[k]);
  * a beam with finished[b, k] != 0 has one candidate, token eos at scores[k], and
  * its logits are not read.  The `beams` best candidates of a batch row, best
- * first, go to scores_out (fp32, rounded once), tokens and parents [batch,
- * beams] (int32; a parent is a beam of the same batch row, 0..beams-1), and
- * finished_out (the parent was finished, or the token is eos).  Within a beam
- * candidates go by logit, then the lower id; between beams by score in 64 bits,
- * then the lower beam.  NaN logits and scores count as -inf; a beam whose logits
- * are all -inf, or hold +inf, has candidates of score -inf.
+ * first, go to scores_out (fp32), tokens and parents [batch, beams] (int32; a
+ * parent is a beam of the same batch row, 0..beams-1), and finished_out (the
+ * parent was finished, or the token is eos).  Within a beam candidates go by
+ * logit, then the lower id; between beams by score, then the lower beam.  The
+ * log-sum-exp of a beam comes from sums in 32 bits: it is within 2^-18 of the
+ * exact one for V up to 65536, whatever the size of the logits, and 2^-23 or so
+ * as a rule.  The rest of a score is formed in 64 bits and rounded once.  So
+ * candidates of two beams that are nearer to each other than those errors may
+ * come in either order, equal logits in another order of the ids among them.
+ * NaN logits and scores count as -inf; a beam whose logits are all -inf, or hold
+ * +inf, has candidates of score -inf.
  * finished and finished_out: both given with eos in [0, V), or both NULL (eos is
  * then -1 and no beam ends).  The outputs may be the inputs' own buffers. */
 #define NC_MAX_BEAMS 32

@@ -166,6 +166,56 @@ def test_select_of_a_large_vocabulary():
     _check(z, s, "fp32")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("size", [30.0, 1e3, 3e4, 1e10, 3e38])
+def test_select_of_large_logits(size, dtype):
+    """The log-sum-exp is exact to the same bound whatever the size of the logits: a shift that is rounded on the way does
+    not show in it."""
+    z, s = _random(3, 4, 4160, 21, spread=1.0)
+    z *= size / z.abs().max()
+    near = torch.linspace(0.0, -6.0, 64)  # candidates of weight beside the largest, where the type tells them apart
+    z[1, :, 100:164] = size + near
+    z[2] = -size + torch.randn(4, 4160, generator=torch.Generator().manual_seed(5))  # and far below zero
+    _check(z, s, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("top", [15.0, 14.8125, 1003.0, 30000.0])
+def test_select_of_beams_with_one_likely_token(top, dtype):
+    """All weight on one id: its score is its beam's, and never above it."""
+    z = torch.full((2, 3, 65536), -100.0)
+    for k in range(3):
+        z[:, k, 501 * k + 77] = top
+    s = torch.tensor([[-1.25, -2.5, -0.75], [0.0, -3.0, -7.0]])
+    _check(z, s, dtype)
+    m = _model(65536, dtype)
+    i = lambda: torch.empty(2, 3, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.empty(2, 3, device="cuda")
+    m.beam_select(z.to(TYPES[dtype]).cuda(), s.cuda(), out, i(), i())
+    assert torch.equal(out.cpu(), s.sort(dim=1, descending=True).values)
+
+
+@pytest.mark.parametrize("size", [1.0, 40.0, 5000.0])
+def test_select_of_beams_with_the_same_logits_in_another_order(size):
+    """Equal beams whose ids are permuted: their candidates tie, and which of them come first is open within the
+    log-sum-exp's bound of 2^-18, but the scores are the K best ones."""
+    g = torch.Generator().manual_seed(3)
+    row = (torch.randn(65536, generator=g) * size).to(torch.bfloat16).float()
+    z = torch.stack([row[torch.randperm(65536, generator=g)] for _ in range(6)])[None].contiguous()
+    s = torch.full((1, 6), -2.0)
+    m = _model(65536)
+    i = lambda: torch.empty(1, 6, dtype=torch.int32, device="cuda")  # noqa: E731
+    out, tok, par = torch.empty(1, 6, device="cuda"), i(), i()
+    m.beam_select(z.bfloat16().cuda(), s.cuda(), out, tok, par)
+    assert m.check() == 0
+    want = _plain(z[0].numpy(), s[0].numpy(), None, -1)[0]
+    assert np.all(np.abs(out[0].cpu().double().numpy() - want) <= 2.0 ** -24 * np.abs(want) + 2.0 ** -18)
+    assert len(set(zip(par[0].tolist(), tok[0].tolist()))) == 6
+    every = -2.0 + torch.log_softmax(z[0].double(), 1)
+    picked = np.array([float(every[p, t]) for p, t in zip(par[0].tolist(), tok[0].tolist())])
+    assert np.all(np.abs(picked - want) <= 2.0 ** -17)  # two beams' errors
+
+
 def test_select_refusals():
     m = _model(512)
     z = torch.zeros(2, 3, 512, dtype=torch.bfloat16, device="cuda")
