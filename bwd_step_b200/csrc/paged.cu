@@ -429,6 +429,12 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restric
     constexpr int WAYS = HD >= 32 ? 1 : 32 / HD;  // keys that a warp's lanes take at once in the second product
     __shared__ float sq[HD], sm[4], sl[4], so[4][HD];
     const int row = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (row == rows) {  // the block behind the rows: every request's length and rows, whether it has any or not
+        int lo, n, len;
+        for (int r = threadIdx.x; h == 0 && r < kv.n_req; r += blockDim.x)
+            if (!request(kv, rows, r, lo, n, len)) set_status(status, ST_BAD_LENGTH);
+        return;
+    }
     const int Nqkv = (H + 2 * nkv) * HD, kvn = nkv * HD;
     A* const kc = reinterpret_cast<A*>(kv.k);
     A* const vc = reinterpret_cast<A*>(kv.v);
@@ -446,12 +452,9 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restric
     for (int c = threadIdx.x; c < HD; c += blockDim.x) sq[c] = tof(qkv[(size_t)row * Nqkv + (size_t)h * HD + c]) * scale_log2;
     if (row < cu[0] || row >= cu[kv.n_req]) return;  // behind the last sequence: stays as it was
     const int r = row_request_warp(cu, kv.n_req, row, lane);
-    const int lo = cu[r], hi = cu[r + 1], all = kv.kv_len[r];
-    const int before = all - (hi - lo);  // positions in the cache
-    if (lo < 0 || hi > rows || before < 0 || all > (long long)kv.max_blocks * kv.page) {
-        if (threadIdx.x == 0 && h == 0) set_status(status, ST_BAD_LENGTH);
-        return;
-    }
+    int lo, fresh, all;
+    if (!request(kv, rows, r, lo, fresh, all)) return;
+    const int before = all - fresh;  // positions in the cache
     __syncthreads();
     const int len = before + (row - lo) + 1;  // keys that the row sees
     const int32_t* table = kv.table + (size_t)r * kv.max_blocks;
@@ -697,7 +700,7 @@ template <typename A>
 cudaError_t attention_simt_t(const void* qkv, int H, int nkv, int hd, int rows, const int32_t* slots, const PagedKv& kv,
                              void* o, int* status, cudaStream_t s) {
     const float sl = 1.44269504088896340736f / sqrtf((float)hd);
-    const dim3 grid(rows, H);
+    const dim3 grid(rows + 1, H);
     const A* q = reinterpret_cast<const A*>(qkv);
     A* out = reinterpret_cast<A*>(o);
     switch (hd) {

@@ -27,6 +27,17 @@ struct PagedKv {
     int n_req, max_blocks, page, n_pages;
 };
 
+// New rows and length of request r; false (nothing to do, or reported) where the
+// step's arrays do not fit each other.
+__device__ __forceinline__ bool request(const PagedKv& kv, int rows, int r, int& lo, int& n, int& len) {
+    lo = kv.cu_rows[r];
+    const int hi = kv.cu_rows[r + 1];
+    len = kv.kv_len[r];
+    n = hi - lo;
+    const long long cap = (long long)kv.max_blocks * kv.page;
+    return lo >= 0 && hi <= rows && n >= 0 && len >= n && len <= cap;
+}
+
 // Block tables, row offsets, positions and slots of a step (see nc_page_plan).
 cudaError_t launch_page_plan(int n_req, int page, int max_blocks, int n_pages, int rows, const int32_t* cached,
                              const int32_t* new_len, const int32_t* release, int32_t* table, int32_t* free_pages,

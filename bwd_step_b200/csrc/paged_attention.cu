@@ -85,17 +85,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 // ---------------------------------------------------------------- requests
-// New rows and length of request r; false (nothing to do, or reported) where the
-// step's arrays do not fit each other.
-__device__ __forceinline__ bool request(const PagedKv& kv, int rows, int r, int& lo, int& n, int& len) {
-    lo = kv.cu_rows[r];
-    const int hi = kv.cu_rows[r + 1];
-    len = kv.kv_len[r];
-    n = hi - lo;
-    const long long cap = (long long)kv.max_blocks * kv.page;
-    return lo >= 0 && hi <= rows && n >= 0 && len >= n && len <= cap;
-}
-
 // Exclusive prefix sums of v(r), r < n, into pre[0..n] by all NT threads of the block.
 template <int NT, typename T, typename F>
 __device__ __forceinline__ void block_prefix(T* pre, int n, F v) {

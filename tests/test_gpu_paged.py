@@ -426,6 +426,21 @@ def test_attention_reports_missing_pages_and_lengths():
     assert m.check() == 0
 
 
+@pytest.mark.parametrize("h,hd,dtype", [(10, 128, "bf16"), (12, 64, "bf16"), (4, 16, "bf16"), (10, 128, "fp32")])
+@pytest.mark.parametrize("length", [1 << 20, -1])
+def test_requests_without_new_rows_have_their_lengths_checked(h, hd, dtype, length):
+    """On every path, and the other requests' rows come out all the same."""
+    m = _model(h, 1, hd, dtype)
+    lens = [(100, 1), (50, 0), (20, 1), (0, 0)]
+    s, t = (Step(h, 1, hd, 16, lens, dtype, seed=1) for _ in range(2))
+    want = t.run(m).clone()
+    assert m.check() == 0
+    s.kv_len[1] = length
+    s.run(m)
+    assert m.check() == _lib.NC_ERR_BAD_LENGTH
+    assert torch.equal(s.o, want)
+
+
 def test_refusals():
     m = _model()
     s = Step(10, 1, 128, 16, [(100, 1), (50, 1)], seed=1)
