@@ -276,8 +276,9 @@ int nc_page_plan(nc_model* m, int n_req, int page_size, int max_blocks, int n_pa
  *   o[i] = softmax(q K^T / sqrt(head_dim)) V into o [rows, n_head head_dim].
  *   Rows from cu_rows[n_req] on are left as they were.
  *   max_new: an upper bound of every request's number of new rows, 0 if none is
- *   known (it chooses the kernels).  A request with more rows than that is
- *   reported as NC_ERR_BAD_LENGTH and may be left without output.  A request whose length or rows do
+ *   known (it chooses the kernels).  On the tensor cores a request with more rows
+ *   than that is reported as NC_ERR_BAD_LENGTH and may be left without output;
+ *   plain FMAs need no bound and compute it.  A request whose length or rows do
  *   not fit the table or the step, with new rows or without, is reported as
  *   NC_ERR_BAD_LENGTH and left without output.
  *   workspace: nc_paged_attention_workspace_bytes(m, n_req, rows) bytes,
