@@ -102,6 +102,18 @@ int i32_of(int64_t v, const char* name) {
     return static_cast<int>(v);
 }
 
+// Calls the library without the interpreter's lock: a launch waits where the stream's queue is full,
+// and the program's other threads go on meanwhile.  The arguments are addresses and sizes by then, taken
+// before the lock is given up; the caller holds the tensors.
+template <typename F, typename... A>
+int unlocked(F* f, A... args) {
+    struct Unlocked {
+        PyThreadState* const state = PyEval_SaveThread();
+        ~Unlocked() { PyEval_RestoreThread(state); }
+    } unlocked;
+    return f(args...);
+}
+
 template <typename F>
 PyObject* call(F f) {
     try {
@@ -136,10 +148,10 @@ PyObject* page_plan(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         shape(slots, {pos.numel()}, "slots");
         if (release) shape(*release, {n}, "release");
         auto p = [&](const at::Tensor& t, const char* name) { return static_cast<int32_t*>(a.address(t, kI32, name)); };
-        return nc_page_plan(a.model, i32_of(n, "new_len"), page, i32_of(table.size(1), "block_table"), i32_of(free.numel(), "free_pages"),
-                            i32_of(pos.numel(), "positions"), p(cached, "cached_len"), p(fresh, "new_len"),
-                            release ? p(*release, "release") : nullptr, p(table, "block_table"), p(free, "free_pages"),
-                            p(count, "free_count"), p(cu, "cu_rows"), p(kv_len, "kv_len"), p(pos, "positions"), p(slots, "slots"), a.pointer());
+        return unlocked(nc_page_plan, a.model, i32_of(n, "new_len"), page, i32_of(table.size(1), "block_table"), i32_of(free.numel(), "free_pages"),
+                        i32_of(pos.numel(), "positions"), p(cached, "cached_len"), p(fresh, "new_len"),
+                        release ? p(*release, "release") : nullptr, p(table, "block_table"), p(free, "free_pages"),
+                        p(count, "free_count"), p(cu, "cu_rows"), p(kv_len, "kv_len"), p(pos, "positions"), p(slots, "slots"), a.pointer());
     });
 }
 
@@ -183,10 +195,10 @@ PyObject* paged_attention(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
             refuse(PyExc_ValueError, "k_pages must be [pages, page_size, n_kv_head, head_dim]");
         shape(v, {k.size(0), k.size(1), nkv, hd}, "v_pages");
         const Step s(a, rows);
-        return nc_paged_attention(a.model, a.address(qkv, type, "qkv"), i32_of(rows, "qkv"), s.n, max_new, s.cu, s.kv_len, s.slots, s.table,
-                                  s.blocks, i32_of(k.size(1), "page_size"), i32_of(k.size(0), "k_pages"), a.address(k, type, "k_pages"),
-                                  a.address(v, type, "v_pages"), a.address(o, type, "o"), a.address(ws, kAny, "workspace"), ws.nbytes(),
-                                  peek.pointer());
+        return unlocked(nc_paged_attention, a.model, a.address(qkv, type, "qkv"), i32_of(rows, "qkv"), s.n, max_new, s.cu, s.kv_len, s.slots, s.table,
+                        s.blocks, i32_of(k.size(1), "page_size"), i32_of(k.size(0), "k_pages"), a.address(k, type, "k_pages"),
+                        a.address(v, type, "v_pages"), a.address(o, type, "o"), a.address(ws, kAny, "workspace"), ws.nbytes(),
+                        peek.pointer());
     });
 }
 
@@ -215,11 +227,11 @@ PyObject* paged_forward(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         check_pages(kv, layers, nkv, hd);
         const Step s(a, rows);
         shape(logits, {s.n, vocab}, "logits");
-        return nc_paged_forward(a.model, static_cast<int32_t*>(a.address(tokens, kI32, "tokens")), i32_of(rows, "tokens"), s.n, max_new,
-                                static_cast<int32_t*>(a.address(pos, kI32, "positions")), s.cu, s.kv_len, s.slots, s.table, s.blocks,
-                                i32_of(kv.size(3), "page_size"), i32_of(kv.size(2), "kv_pages"), a.address(w, type, "weights"),
-                                a.address(kv, type, "kv_pages"), a.address(logits, type, "logits"), a.address(ws, kAny, "workspace"),
-                                ws.nbytes(), peek.pointer());
+        return unlocked(nc_paged_forward, a.model, static_cast<int32_t*>(a.address(tokens, kI32, "tokens")), i32_of(rows, "tokens"), s.n, max_new,
+                        static_cast<int32_t*>(a.address(pos, kI32, "positions")), s.cu, s.kv_len, s.slots, s.table, s.blocks,
+                        i32_of(kv.size(3), "page_size"), i32_of(kv.size(2), "kv_pages"), a.address(w, type, "weights"),
+                        a.address(kv, type, "kv_pages"), a.address(logits, type, "logits"), a.address(ws, kAny, "workspace"),
+                        ws.nbytes(), peek.pointer());
     });
 }
 
@@ -250,7 +262,7 @@ PyObject* beam_select(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         auto* so = static_cast<float*>(a.address(out, kF32, "scores_out"));
         auto p = [&](const at::Tensor* t, const char* name) { return t ? static_cast<int32_t*>(a.address(*t, kI32, name)) : nullptr; };
         int32_t *f = p(fin, "finished"), *fo = p(fin_out, "finished_out"), *to = p(&tokens, "tokens"), *pa = p(&parents, "parents");
-        return nc_beam_select(a.model, z, i32_of(b, "batch"), i32_of(k, "beams"), sc, f, eos, so, to, pa, fo, a.pointer());
+        return unlocked(nc_beam_select, a.model, z, i32_of(b, "batch"), i32_of(k, "beams"), sc, f, eos, so, to, pa, fo, a.pointer());
     });
 }
 
@@ -267,8 +279,8 @@ PyObject* beam_reorder(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         const int64_t b = parents.size(0), k = parents.size(1);
         if ((double)kv.nbytes() < (double)each * b * k * t_max)
             refuse(PyExc_ValueError, "kv_cache smaller than kv_cache_bytes(batch * beams, T_max)");
-        return nc_beam_reorder(a.model, a.address(kv, kAny, "kv_cache"), i32_of(b, "batch"), i32_of(k, "beams"), t_max,
-                               static_cast<int32_t*>(a.address(parents, kI32, "parents")), start, end, a.pointer());
+        return unlocked(nc_beam_reorder, a.model, a.address(kv, kAny, "kv_cache"), i32_of(b, "batch"), i32_of(k, "beams"), t_max,
+                        static_cast<int32_t*>(a.address(parents, kI32, "parents")), start, end, a.pointer());
     });
 }
 
@@ -287,10 +299,10 @@ PyObject* beam_reorder_paged(PyObject*, PyObject* const* args, Py_ssize_t nargs)
         shape(starts, {b * k}, "starts");
         shape(ends, {b * k}, "ends");
         auto p = [&](const at::Tensor& t, const char* name) { return static_cast<int32_t*>(a.address(t, kI32, name)); };
-        return nc_beam_reorder_paged(a.model, a.address(kv, type, "kv_pages"), i32_of(b, "batch"), i32_of(k, "beams"),
-                                     i32_of(kv.size(2), "kv_pages"), i32_of(kv.size(3), "page_size"), p(parents, "parents"),
-                                     p(table, "block_table"), i32_of(table.size(1), "block_table"), p(starts, "starts"), p(ends, "ends"),
-                                     a.pointer());
+        return unlocked(nc_beam_reorder_paged, a.model, a.address(kv, type, "kv_pages"), i32_of(b, "batch"), i32_of(k, "beams"),
+                        i32_of(kv.size(2), "kv_pages"), i32_of(kv.size(3), "page_size"), p(parents, "parents"),
+                        p(table, "block_table"), i32_of(table.size(1), "block_table"), p(starts, "starts"), p(ends, "ends"),
+                        a.pointer());
     });
 }
 

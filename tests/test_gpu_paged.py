@@ -2,6 +2,8 @@
 allocator, attention against 64 bits, the beams' reordering against copies."""
 import math
 import random
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -147,6 +149,38 @@ def test_a_free_page_outside_the_cache_is_reported():
     assert m.check() == _lib.NC_ERR_BAD_PAGE
     assert got[0][0][0] == 1 and got[6][:3] == [16, 17, 18]
     assert got[6][3:] == [-1] * 16 + [32, 33, 34, 35]
+
+
+def test_a_full_launch_queue_leaves_other_threads_running():
+    """Launches wait for room in the stream's queue; the program's other threads go on meanwhile."""
+    m, stream = _model(), torch.cuda.Stream()
+    i = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = (16, i(2), _ints([1, 1]), _ints([[0], [1]]), i(4), i(1), i(3), i(2), i(4), i(4))
+    m.page_plan(*args)
+    torch.cuda.synchronize()
+    gaps, stop = [], threading.Event()
+
+    def beat():
+        last = time.monotonic()
+        while not stop.is_set():
+            time.sleep(0.002)
+            now = time.monotonic()
+            gaps.append(now - last)
+            last = now
+    other = threading.Thread(target=beat)
+    other.start()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(2_000_000_000)  # about a second of the GPU's clock
+    began = time.monotonic()
+    for _ in range(6000):
+        m.page_plan(*args, stream=stream)
+    took = time.monotonic() - began
+    stop.set()
+    other.join()
+    torch.cuda.synchronize()
+    assert m.check() == 0
+    assert took > 0.5, "the queue was not full"
+    assert max(gaps) < 0.25 * took
 
 
 # ---------------------------------------------------------------- attention
