@@ -39,6 +39,8 @@ class PagedCache:
     def plan(self, new_len, rows, release=None, stream=None):
         """Plans a step of new_len [n_req] (device int32) new positions on top of
         kv_len, in `rows` packed rows, after giving back the requests of release."""
+        if not 1 <= rows <= self._positions.numel():
+            raise ValueError(f"rows must be 1 to {self._positions.numel()}, the rows that the cache was made for, got {rows}")
         self.positions, self.slots = self._positions[:rows], self._slots[:rows]
         self.model.page_plan(self.page_size, self.kv_len, new_len, self.block_table, self.free_pages, self.free_count,
                              self.cu_rows, self.kv_len, self.positions, self.slots, release=release, stream=stream)

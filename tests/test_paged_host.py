@@ -6,7 +6,7 @@ import pytest
 
 import bwd_step_b200
 from bwd_step_b200 import Model, _lib
-from bwd_step_b200.generate import beam_search
+from bwd_step_b200.generate import PagedCache, beam_search
 
 torch = pytest.importorskip("torch")
 
@@ -87,3 +87,22 @@ def test_searches_that_cannot_run_are_refused():
     for prompts, beams, new in (([], 2, 1), ([[1], []], 2, 1), ([[1]], 2, 0), ([[1]], 0, 1), ([[1]], 33, 1)):
         with pytest.raises(ValueError):
             beam_search(m, None, prompts, beams, new)
+
+
+def test_a_step_of_more_rows_than_the_cache_was_made_for_is_refused():
+    """Before anything is planned: the cache would claim positions that no forward can write."""
+    calls = []
+    i = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    c = object.__new__(PagedCache)
+    c.model = types.SimpleNamespace(page_plan=lambda *a, **kw: calls.append(a))
+    c.page_size, c.n_req = 16, 2
+    c.kv_len, c.cu_rows, c.block_table, c.free_pages, c.free_count = i(2), i(3), i(4).view(2, 2), i(4), i(1)
+    c._positions, c._slots = i(8), i(8)
+    for rows in (9, 0, -1):
+        with pytest.raises(ValueError, match="rows"):
+            c.plan(i(2), rows)
+    assert not calls
+    for rows in (1, 8):
+        c.plan(i(2), rows)
+        assert c.positions.numel() == c.slots.numel() == rows
+    assert len(calls) == 2
