@@ -1,6 +1,7 @@
 """Builds libnanochat_b200.so in-tree with nvcc for sm_100a.
 
-Also builds _serving.so, the Python binding of the serving calls, against it.
+Also builds _serving.so, the Python binding of the serving calls, against it
+(skipped with a message where PyTorch or g++ is absent; nothing else needs it).
 Each csrc/*.cu is compiled to an object under _build/ (in parallel, only when
 it or a header changed), then all objects are linked into one shared library
 next to this file.  Usage: python -m bwd_step_b200.build [--force] [-v]
@@ -81,12 +82,19 @@ def _build_serving(force: bool, verbose: bool):
     if not force and os.path.exists(SERVING) and os.path.getmtime(SERVING) >= newest:
         return
     import sysconfig
-
-    import torch
+    try:
+        import torch
+    except ImportError:
+        print("serving binding not built: PyTorch is absent", file=sys.stderr)
+        return
+    cxx = shutil.which("g++")
+    if cxx is None:
+        print("serving binding not built: g++ is absent", file=sys.stderr)
+        return
     root = os.path.dirname(torch.__file__)
     inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
-    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    cmd = [cxx, "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-DUSE_CUDA", *[f"-I{d}" for d in inc], src, "-o", SERVING, f"-L{HERE}", "-lnanochat_b200", "-Wl,-rpath,$ORIGIN",
            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
