@@ -77,10 +77,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
 
 def _build_serving(force: bool, verbose: bool):
-    src = os.path.join(CSRC, "serving_py.cpp")
-    newest = max(os.path.getmtime(f) for f in [src] + glob.glob(os.path.join(INCLUDE, "*.h")))
-    if not force and os.path.exists(SERVING) and os.path.getmtime(SERVING) >= newest:
-        return
+    """Where the source, a header, PyTorch or Python has changed: the binding uses PyTorch's and Python's internals, so
+    one built for others may not load, or load and misread them.  What it was built for stands beside it."""
     import sysconfig
     try:
         import torch
@@ -91,10 +89,19 @@ def _build_serving(force: bool, verbose: bool):
     if cxx is None:
         print("serving binding not built: g++ is absent", file=sys.stderr)
         return
+    src = os.path.join(CSRC, "serving_py.cpp")
+    newest = max(os.path.getmtime(f) for f in [src] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    made_for = f"torch {torch.__version__}, C++ ABI {abi}, {sysconfig.get_config_var('SOABI')}\n"
+    stamp = SERVING + ".for"
+    if not force and os.path.exists(SERVING) and os.path.getmtime(SERVING) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made_for:
+                return
     root = os.path.dirname(torch.__file__)
     inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"]]
-    cmd = [cxx, "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+    cmd = [cxx, "-std=c++17", "-O2", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
            "-DUSE_CUDA", *[f"-I{d}" for d in inc], src, "-o", SERVING, f"-L{HERE}", "-lnanochat_b200", "-Wl,-rpath,$ORIGIN",
            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
@@ -102,6 +109,8 @@ def _build_serving(force: bool, verbose: bool):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"building {SERVING} failed:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(made_for)
 
 
 if __name__ == "__main__":
