@@ -7,6 +7,7 @@ dtype, device and contiguity.
 from __future__ import annotations
 
 import ctypes
+import os
 
 from . import _lib
 from ._lib import NcConfig, lib
@@ -56,6 +57,10 @@ def _serving():
         try:
             from . import _serving as module
         except ImportError as e:
+            from . import build
+            if os.path.exists(build.SERVING):
+                raise RuntimeError(f"bwd_step_b200: the serving binding does not load ({e}); build it again with "
+                                   "`python -m bwd_step_b200.build --force`") from e
             raise RuntimeError("bwd_step_b200: the serving binding is missing; build it with `python -m bwd_step_b200.build` "
                                "(or __graft_entry__.build())") from e
         _serving_module = module

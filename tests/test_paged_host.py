@@ -1,5 +1,6 @@
 """Checks of the paged-cache and beam-search calls that need no GPU: what the
 binding and the library refuse before anything runs on a device."""
+import sys
 import types
 
 import pytest
@@ -106,3 +107,17 @@ def test_a_step_of_more_rows_than_the_cache_was_made_for_is_refused():
         c.plan(i(2), rows)
         assert c.positions.numel() == c.slots.numel() == rows
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("present", [False, True])
+def test_a_binding_that_is_missing_and_one_that_does_not_load_are_told_apart(present, tmp_path, monkeypatch):
+    from bwd_step_b200 import api, build
+    if present:
+        (tmp_path / "_serving.so").write_bytes(b"no library")
+    monkeypatch.setattr(build, "SERVING", str(tmp_path / "_serving.so"))
+    monkeypatch.setattr(bwd_step_b200, "__path__", [str(tmp_path)])  # where the package's modules are looked for
+    monkeypatch.delattr(bwd_step_b200, "_serving", raising=False)
+    monkeypatch.delitem(sys.modules, "bwd_step_b200._serving", raising=False)
+    monkeypatch.setattr(api, "_serving_module", None)
+    with pytest.raises(RuntimeError, match="does not load.*file too short|does not load.*invalid ELF" if present else "is missing"):
+        api._serving()
