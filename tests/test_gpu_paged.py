@@ -554,6 +554,32 @@ def test_paged_reorder(beams, page):
     assert torch.equal(kv, want) and m.check() == 0
 
 
+@pytest.mark.parametrize("beams,page", [(2, 16), (3, 32), (5, 16), (8, 64), (9, 16), (20, 32), (32, 16)])
+@pytest.mark.parametrize("dtype,nkv,hd", [("bf16", 1, 64), ("fp32", 2, 32), ("fp32", 1, 128)])
+def test_paged_reorder_with_a_span_for_every_beam(beams, page, dtype, nkv, hd):
+    """The spans of a row's beams differ, empty ones among them; a parent gives what it held before the call."""
+    m = _model(2 * nkv, nkv, hd, dtype, layers=2)
+    batch, rng = 3, random.Random(beams * 5 + page)
+    g = torch.Generator(device="cuda").manual_seed(beams)
+    starts = [rng.randint(0, 70) for _ in range(batch * beams)]
+    ends = [max(0, a + rng.choice([0, -3, 1, rng.randint(0, 80), rng.randint(0, 80)])) for a in starts]
+    width = -(-max(max(starts), max(ends)) // page) + 1
+    n_pages = batch * beams * width + 1
+    perm = list(range(n_pages))
+    rng.shuffle(perm)
+    table = [[perm.pop() for _ in range(width)] for _ in range(batch * beams)]
+    kv = torch.randn(2, 2, n_pages, page, nkv, hd, generator=g, device="cuda").to(TYPES[dtype])
+    parents = [[rng.randrange(beams) for _ in range(beams)] for _ in range(batch)]
+    want = kv.clone()
+    for b in range(batch):
+        for i, par in enumerate(parents[b]):
+            row, source = table[b * beams + i], table[b * beams + par]
+            for p in range(starts[b * beams + i], ends[b * beams + i]):
+                want[:, :, row[p // page], p % page] = kv[:, :, source[p // page], p % page]
+    m.beam_reorder_paged(kv, _ints(parents), _ints(table), _ints(starts), _ints(ends))
+    assert torch.equal(kv, want) and m.check() == 0
+
+
 def test_reorder_refusals_and_reports():
     m = _model(2, 1, 64, "bf16", layers=2)
     cache = torch.zeros(2, 2, 4, 8, 1, 64, dtype=torch.bfloat16, device="cuda")
