@@ -433,6 +433,24 @@ def test_calls_at_once_on_two_streams():
         assert torch.equal(s.o, w)
 
 
+@pytest.mark.parametrize("h,hd", [(10, 128), (12, 64), (4, 16)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_row_that_is_not_finite_stays_in_its_request(h, hd, value):
+    """A new v that is not finite: every later row of its request sees it; no other request's row, no decoding
+    request's, and no row 256 or more before it changes by a bit."""
+    lens = [(20, 300), (33, 50), (70, 1), (5, 1)]
+    m = _model(h, 1, hd)
+    s, t = (Step(h, 1, hd, 16, lens, seed=11) for _ in range(2))
+    want = t.run(m).clone()
+    bad = 290
+    s.qkv.view(s.rows, h + 2, hd)[bad, h + 1] = value
+    s.run(m)
+    assert m.check() == 0
+    assert not torch.isfinite(s.o[bad:300]).any()
+    assert torch.equal(s.o[300:], want[300:])
+    assert torch.equal(s.o[:bad - 255], want[:bad - 255])
+
+
 @pytest.mark.parametrize("h,hd", [(10, 128), (4, 16)])
 def test_a_request_with_more_rows_than_max_new_is_reported(h, hd):
     m = _model(h, 1, hd)
