@@ -20,8 +20,10 @@
 // the product rounded; the mean of |d| over the terms by their weight is at most ln V) and by 2^-22
 // (ex2.approx), each change of the maximum on its way by 5 2^-24, each sum by 2^-24: some 60 2^-24 in
 // all for 65536 ids, so the log-sum-exp is within 2^-18 whatever the size of the logits.
-// One launch, no workspace.  64 x 8 beams of 65536 ids (62 MB) take 27 us: the stream
-// 11.5, bound by HBM, and what follows it by the latency of its steps; 1 x 4 beams 11.5 us.
+// One launch, no workspace.  64 x 8 beams of 65536 ids (62 MB) take 28 us (25.8 in a graph): the
+// stream 11.5, bound by HBM, and what follows it by the latency of its steps; 1 x 4 beams 12 us (9.6).
+// The slow way that many equal or masked candidates take (more than 256 that reach the bound, as where
+// 40 ids are left of 65536) is K passes: 64 x 8 beams 1.0 ms, a vocabulary masked throughout 1.1 ms.
 #include "paged.h"
 #include "tc_common.cuh"
 
@@ -37,7 +39,7 @@ constexpr int kChunk = 16384;  // bytes of a beam's logits brought at once
 constexpr int kStages = 2;     // chunks on their way: at four blocks an SM, 128 KB
 constexpr int kCand = 256;     // gathered candidates; more (many alike) take the slow way
 // Blocks of a cluster, at most.  1x4 beams of 65536 ids: 12.4 us with 4, 9.2 with 8, 9.4 with 16;
-// 64x8 beams: 24.9, 24.6, 51 us.
+// 64x8 beams: 24.9, 24.6, 51 us.  Smaller vocabularies take fewer (see launch_beam_select).
 constexpr int kCluster = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 typedef unsigned long long u64;
@@ -452,6 +454,9 @@ cudaError_t launch_beam_select(DType at, const void* logits, int batch, int beam
     a.scores = scores; a.finished = finished;
     a.scores_out = scores_out; a.tokens = tokens; a.parents = parents; a.finished_out = finished_out;
     a.status = status;
+    // A small vocabulary gains nothing by more blocks, and many rows pay for each.  Graph times, us, with 1, 2, 4, 8 blocks:
+    // 1 x 4 beams of 1024 ids 8.6, 8.9, 8.9, 9.0, of 4096 9.2, 8.9, 8.6, 8.8, of 16384 12.5, 9.8, 9.1, 9.0; 64 x 8 beams of 1024
+    // ids 14.1, 14.7, 15.6, 18.9, of 4096 14.6, 13.8, 14.4, 18.5, of 16384 21.4, 15.3, 15.9, 20.2 (few rows decide from 8192 on).
     const int cluster = V >= 8192 ? kCluster : V >= 4096 ? 4 : V >= 2048 ? 2 : 1;
     a.slice = ((V + cluster - 1) / cluster + 7) & ~7;
     return at == DT_BF16 ? select_t<bf16>(logits, a, cluster, s) : select_t<float>(logits, a, cluster, s);

@@ -115,8 +115,13 @@ __device__ __forceinline__ void plan_row(const PlanArgs& p, const int* cu, const
 // has its loads on their way together: a thread's requests with up to kPlanOwn blocks
 // each, and for the others (long chunks, released requests) a warp with kPlanWide
 // blocks of kPlanKept requests, whose table entries it keeps to the end.  512 requests,
-// 48 of them with chunks and 32 released: 16.4 us (34.6 with one window at a time);
-// four decoding requests: 2.9 us in a graph (3.7 with 1024 threads).
+// 48 of them with chunks and 32 released: 16.6 us, 15.7 in a graph (14.3 where the step was
+// planned before and few pages move; 34.6 with one window at a time); four decoding
+// requests, two of them onto a new page: 3.3 us in a graph, 2.8 where none takes one (3.7
+// with 1024 threads).
+// The kept entries are what 64 registers a thread hold: three requests a warp of up to 256
+// blocks, so 96 chunks and released requests.  Those behind them, and longer rows, are
+// read again in each stage: 250 of 512 requests 28 us, 450 of them 41.
 constexpr int kPlanWide = 8 * 32, kPlanKept = 3;
 constexpr int kPlanSmall = 128;  // requests that a block of as many threads plans
 
@@ -419,7 +424,9 @@ __device__ __forceinline__ int row_request_warp(const int32_t* __restrict__ cu, 
 // own output dims while the 32 weights pass by shuffles.  The four warps are joined at
 // the end.  The step's own keys and values are read from its rows, not from the cache,
 // so the same launch writes them there.  Bound by latency at the sizes of such models
-// (five requests of up to 110 positions, 4 fp32 heads of 16: 7.6 us a call, 5.8 in a graph).
+// (five requests of up to 110 positions, 4 fp32 heads of 16: 7.5 us a call, 5.5 in a graph).
+// No key is shared between rows or heads: prompts of 4 x 256 rows on 512 positions take 65 us, with
+// 10 heads of 128 1014.
 template <typename A, int HD>
 __global__ void __launch_bounds__(128) paged_attention_kernel(const A* __restrict__ qkv, int H, int nkv, int rows,
                                                               const int32_t* __restrict__ slots, const PagedKv kv,

@@ -2,8 +2,8 @@
 //
 // Chunks (two new tokens or more) run on tcgen05 in tiles of 128 rows, a row being a
 // (token, query head).  Bound by the cycle scores -> softmax -> output of a tile: two
-// chunks of some 2000 rows on 5500 positions, 10 heads of 128, take 143 to 153 us (126
-// GFLOP, 820 to 880 TFLOP/s).
+// chunks of some 2000 rows on 5500 positions, 10 heads of 128, take 143 to 155 us, as the
+// power limit lets the clock be (126 GFLOP, 815 to 880 TFLOP/s).
 // Decoding requests (one new token): per K/V head the group's query heads, 16 at
 // most, are the rows of one small matrix product against every cached key, so
 // each key and value is read once for all of them.  Bound by HBM: 128 requests of 900
@@ -26,9 +26,11 @@ using namespace tc;
 
 constexpr int kTile = 64;        // keys of a decode tile
 // Where the table has no more positions than this, nothing is cut over blocks and there is nothing to
-// join.  Steps with chunks: 8 prompts of some 225 rows on up to 700 positions save 4.7 us of the 31.6
-// that they take when cut.  Steps of decoding requests alone, whose join is most of what they do: four requests of up to
-// 700 positions take 12.4 us whole and 10.3 cut, so only tables of a few tiles.
+// join.  Graph times, whole / cut, us, 10 heads of 128:
+//   steps with chunks of some 225 rows on up to 700 positions: 8 requests 27 / 35, 64 requests 109 / 117;
+//   one alone on 600 to 700 positions 27 / 22, the one case here that cutting would serve;
+//   steps of decoding requests alone, 4 and 148 of them: table of 128 positions 6.3 / 7.8 and 8.0 / 8.2, of 256
+//   7.6 / 7.7 and 12.2 / 13.7, of 512 9.5 / 8.4 and 15.6 / 17.2, of 1024 13.2 / 8.7 and 24.6 / 22.6.
 constexpr int kWholePositions = 1024, kWholeDecoding = 256;
 constexpr int kDecRows = 16;     // query heads of a K/V head that the decode kernel takes
 constexpr int kDecThreads = 320; // 8 consumer warps, the producer, and one that writes the cache
@@ -194,8 +196,8 @@ __device__ __forceinline__ uint32_t dec_at(int key, int j, int pshift) {
 // Eight consumer warps in two groups that take the tiles in turn; a warp has 16 of
 // its tile's 64 keys, a running maximum and sum, and a whole output, and the eight are
 // joined at the end of a piece.  S = Q K^T and O += P V are mma.sync products of
-// 16 rows: at 16 rows a tile's 64 KB of operands take 1400 cycles to arrive and
-// some 300 to multiply, and tcgen05's 128 rows would be an eighth full.
+// 16 rows: a tile's 32 KB of operands (head size 128) take 1400 cycles to arrive at an
+// SM's share of the bandwidth and some 300 to multiply, and tcgen05's 128 rows would be an eighth full.
 template <int HD>
 __global__ void __launch_bounds__(kDecThreads, 1)
 paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
@@ -531,11 +533,15 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 //   warps 0-3  softmax of half a, warps 4-7 of half b: a row per thread, running maximum
 //              in the log2 domain that moves only when it grows by 2^8, P as packed bf16.
 // A half's scores, softmax and output wait for each other; the other half's run meanwhile.
-// Both take some 2900 cycles a tile, where the products alone take 2048 and the softmax of
-// both halves 2000.
-constexpr int kChunkThreads = 320;  // softmax of half a, of half b (a warpgroup each); producer, MMA, two idle warps
+// Both take some 3200 cycles a tile (long chunks, 55 tiles a block), where the products alone take 2048
+// and the softmax of both halves 2000.  That is 176 thousand of a block's 207 thousand cycles; its start
+// takes 9, the pieces' first copies and products 11 and their output 11.
+constexpr int kChunkThreads = 320;  // softmax of half a, of half b (a warpgroup each); producer, MMA
 constexpr int kChunkRows = 256;
-constexpr int kWholeTiles = 10;  // units of so many key tiles are not cut: 8 requests of some 900 positions 33.9 -> 30.5 us
+// Units of so many key tiles are not cut: 8 requests of some 900 positions 33.9 -> 30.5 us.  The rule does not ask
+// how many units there are: chunks of 20 rows on 1200 positions take, whole / cut, 36.3 / 37.1 us for 64 requests, but
+// 31.5 / 20.9 for 8 and 30.1 / 18.5 for one, in whose ten tiles one SM walks while the others idle.
+constexpr int kWholeTiles = 10;
 
 struct ChunkArgs {
     PagedKv kv;
@@ -570,8 +576,9 @@ struct ChunkLayout {
 };
 static_assert(ChunkLayout<128>::bytes(kMaxRequests) <= 232448, "chunk shared memory exceeds the per-block limit");
 
-// sum of floor((a i + b) / 128) over i < n, for a <= 256: the whole parts are taken out, then what
-// is left counts the lattice points under a line, whose axes are exchanged until none is.
+// sum of floor((a i + b) / 128) over i < n, for a <= 256 (the floor sum of an arithmetic progression, by
+// the Euclidean algorithm): the whole parts are taken out, then what is left counts the lattice points
+// under a line, whose axes are exchanged until none is.
 __device__ __forceinline__ long long floor_sum128(unsigned n, unsigned a, unsigned b) {
     long long sum = (long long)n * (b >> 7);
     unsigned m = 128;

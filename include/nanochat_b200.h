@@ -231,8 +231,9 @@ int nc_decode_step(nc_model* m, const int32_t* tokens, int B, int pos, const voi
  * page_size: 16, 32, 64, 128 or 256.  block_table: device int32 [n_req,
  * max_blocks], -1 (or any value outside [0, n_pages)) where a block has no
  * page.  n_req <= 4096; max_blocks * page_size and n_pages * page_size at most
- * 2^30, n_req * n_kv_head * max_blocks * page_size about 2^37.  A position that a step writes must be in a page of its own: requests
- * may share a page only where none of them writes.
+ * 2^30, n_req * n_kv_head * max_blocks * page_size about 2^37.  A position that
+ * a step writes must be in a page of its own: requests may share a page only
+ * where none of them writes.
  *
  * nc_page_plan builds what a step of n_req requests needs from their lengths, on
  * the GPU:
@@ -246,8 +247,9 @@ int nc_decode_step(nc_model* m, const int32_t* tokens, int B, int pos, const voi
  *     free pages as a stack, its top last.  Released pages are pushed in the
  *     order of requests and blocks, then every block of [cached_len,
  *     cached_len + new_len) without a page takes one from the top, in that
- *     order.  Blocks that have a page keep it, so planning a step twice changes
- *     nothing.
+ *     order.  Blocks that have a page keep it, so planning a step without
+ *     releases twice changes nothing (released requests would give back the pages
+ *     that they took, and take them in another order).
  *   cu_rows [n_req + 1]: packed row of every request's first new token, and the
  *     number of rows in use; kv_len [n_req]: cached + new (may be cached_len's
  *     own buffer).
@@ -286,7 +288,10 @@ int nc_page_plan(nc_model* m, int n_req, int page_size, int max_blocks, int n_pa
  *   calls that may run at once (two streams, two graphs) need one each.
  * A block without a page inside a request's length reads as zeros and is
  * reported as NC_ERR_BAD_PAGE.  Cache contents past a request's length are not
- * used, whatever they are.  Results are bitwise reproducible for the same
+ * used, whatever they are.  The step's own v should be finite: on the tensor
+ * cores a new v that is not reaches, beside the rows behind it, up to 255 rows
+ * of its request before it (their weight for it is 0, and 0 times it is NaN); no
+ * other request sees it.  Results are bitwise reproducible for the same
  * lengths, table width and max_new.  bf16 models with head_dim 64 or 128 and at
  * most 128 query heads per K/V head run on the tensor cores (requests with one new
  * row and at most 16 such heads on a kernel of their own), others on plain FMAs. */
