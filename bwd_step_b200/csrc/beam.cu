@@ -19,7 +19,8 @@
 // The sums are kept in 32 bits.  A term e^d is off by 2.3 |d| 2^-24 of itself (the difference, the factor and
 // the product rounded; the mean of |d| over the terms by their weight is at most ln V) and by 2^-22
 // (ex2.approx), each change of the maximum on its way by 5 2^-24, each sum by 2^-24: some 60 2^-24 in
-// all for 65536 ids, so the log-sum-exp is within 2^-18 whatever the size of the logits.
+// all for 65536 ids, so the log-sum-exp is within 2^-18 whatever the size of the logits.  Measured over
+// normal logits of deviations 0.01 to 1000, 4160 to 262400 ids: 1.2 2^-24 root mean square, 4.4 2^-24 at most.
 // One launch, no workspace.  64 x 8 beams of 65536 ids (62 MB) take 28 us (25.8 in a graph): the
 // stream 11.5, bound by HBM, and what follows it by the latency of its steps; 1 x 4 beams 12 us (9.6).
 // The slow way that many equal or masked candidates take (more than 256 that reach the bound, as where

@@ -324,7 +324,7 @@ int nc_paged_forward(nc_model* m, const int32_t* tokens, int rows, int n_req, in
  * parent was finished, or the token is eos).  Within a beam candidates go by
  * logit, then the lower id; between beams by score, then the lower beam.  The
  * log-sum-exp of a beam comes from sums in 32 bits: it is within 2^-18 of the
- * exact one for V up to 65536, whatever the size of the logits, and 2^-23 or so
+ * exact one for V up to 65536, whatever the size of the logits, and within 2^-21
  * as a rule.  The rest of a score is formed in 64 bits and rounded once.  So
  * candidates of two beams that are nearer to each other than those errors may
  * come in either order, equal logits in another order of the ids among them.
